@@ -58,6 +58,18 @@ SIGNATURES = {
     "moe_layer_workspace_size": (_I, [_I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
     "moe_layer_forward": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _Z,
                                _P, _S]),
+    "moe_gated_ffn_forward_workspace_size": (_I, [_I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_gated_ffn_forward": (_I, [_P, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P, _Z, _P, _S]),
+    "moe_gated_ffn_backward_workspace_size": (_I, [_I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_gated_ffn_backward": (_I, [_P, _I, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _Z, _P,
+                                    _S]),
+    "moe_linear_ce_forward_workspace_size": (_I, [_I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_linear_ce_forward": (_I, [_P, _I, _P, _P, _I, _I, _I, _I, _P, _P, _P, _Z, _P, _S]),
+    "moe_linear_ce_backward_workspace_size": (_I, [_I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_linear_ce_backward": (_I, [_P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _Z, _P,
+                                    _S]),
+    "moe_grad_norm_clip_workspace_size": (_I, [_I, ctypes.POINTER(ctypes.c_size_t)]),
+    "moe_grad_norm_clip": (_I, [_P, _P, _P, _I, ctypes.c_float, _P, _P, _P, _Z, _P, _S]),
 }
 
 _lib = None
@@ -518,3 +530,249 @@ def layer_forward(X, logits, k, renormalize, packed_gu, absmax_gu, packed_d, abs
         _ptr(absmax_gu), _ptr(packed_d), _ptr(absmax_d), _ptr(out), _ptr(workspace),
         workspace.numel(), _ptr(dev_err), _stream(X.device)), "moe_layer_forward")
     return out
+
+
+# ---- the dense training-side operators
+#
+# Their tensors must lie on one device; the launches are made with that device
+# current, whatever the caller's current device is.
+
+
+_HALF = (torch.bfloat16, torch.float16)
+
+
+class _on:
+    """``with _on(device)``: the device of the tensors is current."""
+
+    def __init__(self, device):
+        self.guard = None
+        if device.type == "cuda" and device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _matrix(t, shape, name, dtype, device):
+    """``t`` is a contiguous tensor of exactly this shape, type and device."""
+    if t is None:
+        return
+    _need(t, dtype, name)
+    if t.shape != shape:
+        raise MoEError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != device:
+        raise MoEError(f"{name} is on {t.device}, the call's tensors are on {device}")
+
+
+def _dev_word(dev_err, device):
+    if dev_err is not None:
+        _room(dev_err, 1, "dev_err", (torch.int32,))
+        if dev_err.device != device:
+            raise MoEError(f"dev_err is on {dev_err.device}, the call's tensors are on {device}")
+
+
+def _size(fn, *args):
+    n = ctypes.c_size_t()
+    _check(getattr(load(), fn)(*args, ctypes.byref(n)), fn)
+    return n.value
+
+
+def _space(workspace, nbytes, device):
+    if workspace is None:
+        return torch.empty((max(nbytes, 256),), dtype=torch.uint8, device=device)
+    _room(workspace, nbytes, "workspace", (torch.uint8,))
+    if workspace.device != device:
+        raise MoEError(f"workspace is on {workspace.device}, the call's tensors are on {device}")
+    return workspace
+
+
+def gated_ffn_forward_workspace_size(T, H, I):
+    return _size("moe_gated_ffn_forward_workspace_size", T, H, I)
+
+
+def gated_ffn_backward_workspace_size(T, H, I):
+    return _size("moe_gated_ffn_backward_workspace_size", T, H, I)
+
+
+def _ffn_shapes(X, W_gu, W_d):
+    if not isinstance(X, torch.Tensor) or X.dtype not in _HALF:
+        raise MoEError("X must be a bf16 or fp16 tensor")
+    _need(X, X.dtype, "X", 2)
+    _need(W_d, X.dtype, "W_d", 2)
+    T, H = X.shape
+    I = W_d.shape[1]
+    _matrix(W_d, (H, I), "W_d", X.dtype, X.device)
+    _matrix(W_gu, (2 * I, H), "W_gu", X.dtype, X.device)
+    return T, H, I
+
+
+def gated_ffn_forward(X, W_gu, W_d, residual=None, save_gu=False, workspace=None, out=None,
+                      gu=None, dev_err=None):
+    """Dense gated feed-forward block: ``Y = (silu(X Wg^T) * (X Wu^T)) W_d^T
+    (+ residual)`` with ``X [T, H]``, ``W_gu [2I, H]`` (gate rows, then up),
+    ``W_d [H, I]``, all bf16 or all fp16, ``residual`` fp32 ``[T, H]``.
+    Returns ``Y [T, H]``, or ``(Y, gu)`` when ``save_gu`` or ``gu`` asks for the
+    pre-activations ``[T, 2I]`` that the backward call reads."""
+    T, H, I = _ffn_shapes(X, W_gu, W_d)
+    dev = X.device
+    _matrix(residual, (T, H), "residual", torch.float32, dev)
+    _matrix(out, (T, H), "out", X.dtype, dev)
+    _matrix(gu, (T, 2 * I), "gu", X.dtype, dev)
+    _dev_word(dev_err, dev)
+    with _on(dev):
+        ws = _space(workspace, gated_ffn_forward_workspace_size(T, H, I), dev)
+        if out is None:
+            out = torch.empty((T, H), dtype=X.dtype, device=dev)
+        if gu is None and save_gu:
+            gu = torch.empty((T, 2 * I), dtype=X.dtype, device=dev)
+        _check(load().moe_gated_ffn_forward(
+            _ptr(X), DT[X.dtype], _ptr(W_gu), _ptr(W_d), T, H, I, _ptr(residual), _ptr(out),
+            _ptr(gu), _ptr(ws), ws.numel(), _ptr(dev_err), _stream(dev)), "moe_gated_ffn_forward")
+    return out if gu is None else (out, gu)
+
+
+def gated_ffn_backward(dY, X, gu, W_gu, W_d, need_dx=True, need_dw=True, workspace=None,
+                       dev_err=None):
+    """Gradients of ``gated_ffn_forward`` from ``dY [T, H]`` and its ``gu``:
+    ``(dX [T, H], dW_gu [2I, H], dW_d [H, I])`` of the inputs' type; ``None`` for
+    what ``need_dx`` / ``need_dw`` leave out."""
+    T, H, I = _ffn_shapes(X, W_gu, W_d)
+    dev = X.device
+    _matrix(dY, (T, H), "dY", X.dtype, dev)
+    _matrix(gu, (T, 2 * I), "gu", X.dtype, dev)
+    _dev_word(dev_err, dev)
+    if not (need_dx or need_dw):
+        raise MoEError("gated_ffn_backward: no gradient is asked for")
+    with _on(dev):
+        ws = _space(workspace, gated_ffn_backward_workspace_size(T, H, I), dev)
+        dX = torch.empty_like(X) if need_dx else None
+        dW_gu = torch.empty_like(W_gu) if need_dw else None
+        dW_d = torch.empty_like(W_d) if need_dw else None
+        _check(load().moe_gated_ffn_backward(
+            _ptr(dY), DT[X.dtype], _ptr(X), _ptr(gu), _ptr(W_gu), _ptr(W_d), T, H, I, _ptr(dX),
+            _ptr(dW_gu), _ptr(dW_d), _ptr(ws), ws.numel(), _ptr(dev_err), _stream(dev)),
+            "moe_gated_ffn_backward")
+    return dX, dW_gu, dW_d
+
+
+def linear_ce_forward_workspace_size(T, H, V):
+    return _size("moe_linear_ce_forward_workspace_size", T, H, V)
+
+
+def linear_ce_backward_workspace_size(T, H, V):
+    return _size("moe_linear_ce_backward_workspace_size", T, H, V)
+
+
+def _ce_shapes(X, W, targets):
+    if not isinstance(X, torch.Tensor) or X.dtype not in _HALF:
+        raise MoEError("X must be a bf16 or fp16 tensor")
+    _need(X, X.dtype, "X", 2)
+    _need(W, X.dtype, "W", 2)
+    T, H = X.shape
+    V = W.shape[0]
+    _matrix(W, (V, H), "W", X.dtype, X.device)
+    _matrix(targets, (T,), "targets", torch.int32, X.device)
+    return T, H, V
+
+
+def linear_ce_forward(X, W, targets, ignore_index=-100, workspace=None, dev_err=None):
+    """Cross entropy of the softmax over ``X W^T`` without keeping it: ``X [T,
+    H]``, ``W [V, H]`` (both bf16 or both fp16), ``targets`` int32 ``[T]`` ->
+    ``(loss fp32 [T], lse fp32 [T])``, both 0 in rows whose target is
+    ``ignore_index``."""
+    T, H, V = _ce_shapes(X, W, targets)
+    dev = X.device
+    _dev_word(dev_err, dev)
+    with _on(dev):
+        ws = _space(workspace, linear_ce_forward_workspace_size(T, H, V), dev)
+        loss = torch.empty((T,), dtype=torch.float32, device=dev)
+        lse = torch.empty((T,), dtype=torch.float32, device=dev)
+        _check(load().moe_linear_ce_forward(
+            _ptr(X), DT[X.dtype], _ptr(W), _ptr(targets), T, H, V, ignore_index, _ptr(loss),
+            _ptr(lse), _ptr(ws), ws.numel(), _ptr(dev_err), _stream(dev)),
+            "moe_linear_ce_forward")
+    return loss, lse
+
+
+def linear_ce_backward(dloss, X, W, targets, lse, ignore_index=-100, need_dx=True, need_dw=True,
+                       workspace=None, dev_err=None):
+    """Gradients of ``linear_ce_forward`` for the upstream ``dloss`` fp32
+    ``[T]`` and the forward's ``lse``: ``(dX [T, H], dW [V, H])`` of the inputs'
+    type; ``None`` for what ``need_dx`` / ``need_dw`` leave out."""
+    T, H, V = _ce_shapes(X, W, targets)
+    dev = X.device
+    _matrix(dloss, (T,), "dloss", torch.float32, dev)
+    _matrix(lse, (T,), "lse", torch.float32, dev)
+    _dev_word(dev_err, dev)
+    if not (need_dx or need_dw):
+        raise MoEError("linear_ce_backward: no gradient is asked for")
+    with _on(dev):
+        ws = _space(workspace, linear_ce_backward_workspace_size(T, H, V), dev)
+        dX = torch.empty_like(X) if need_dx else None
+        dW = torch.empty_like(W) if need_dw else None
+        _check(load().moe_linear_ce_backward(
+            _ptr(dloss), _ptr(X), DT[X.dtype], _ptr(W), _ptr(targets), _ptr(lse), T, H, V,
+            ignore_index, _ptr(dX), _ptr(dW), _ptr(ws), ws.numel(), _ptr(dev_err), _stream(dev)),
+            "moe_linear_ce_backward")
+    return dX, dW
+
+
+class GradList:
+    """The gradients of a model as ``grad_norm_clip`` takes them: the host
+    arrays of addresses, sizes and types, built once and used every step.  It
+    holds the tensors, so the addresses stay valid."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = None if outs is None else list(outs)
+        n = len(self.grads)
+        if n == 0:
+            raise MoEError("grad_list: no tensors")
+        if self.outs is not None and len(self.outs) != n:
+            raise MoEError("grad_list: one out per gradient")
+        self.device = self.grads[0].device
+        for i, g in enumerate(self.grads):
+            if g.dtype not in DT:
+                raise MoEError(f"grads[{i}] must be fp32, bf16 or fp16, got {g.dtype}")
+            _matrix(g, g.shape, f"grads[{i}]", g.dtype, self.device)
+            if self.outs is not None:
+                _matrix(self.outs[i], g.shape, f"outs[{i}]", g.dtype, self.device)
+        self.n = n
+        self._in = (ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads])
+        self._numel = (ctypes.c_int64 * n)(*[g.numel() for g in self.grads])
+        self._dt = (ctypes.c_int * n)(*[DT[g.dtype] for g in self.grads])
+        self._out = None if self.outs is None else \
+            (ctypes.c_void_p * n)(*[o.data_ptr() for o in self.outs])
+        self.nbytes = _size("moe_grad_norm_clip_workspace_size", n)
+
+
+def grad_list(grads, outs=None):
+    """A ``GradList`` of contiguous fp32 / bf16 / fp16 tensors; ``outs``: where
+    the clipped gradients go (default: in place)."""
+    return GradList(grads, outs)
+
+
+def grad_norm_clip(grads, max_norm, norm=None, workspace=None, dev_err=None):
+    """Global 2-norm of ``grads`` (a ``GradList``, or tensors) and clipping by
+    it: each becomes ``g * min(1, max_norm / (norm + 1e-6))``, in place or in
+    the list's ``outs``.  Returns the norm, fp32 ``[1]`` on the device.  A norm
+    that is not finite leaves the gradients as they are and sets
+    ``DEVERR_NONFINITE``."""
+    if not isinstance(grads, GradList):
+        grads = GradList(grads)
+    dev = grads.device
+    _matrix(norm, (1,), "norm", torch.float32, dev)
+    _dev_word(dev_err, dev)
+    with _on(dev):
+        ws = _space(workspace, grads.nbytes, dev)
+        if norm is None:
+            norm = torch.empty((1,), dtype=torch.float32, device=dev)
+        _check(load().moe_grad_norm_clip(
+            grads._in, grads._numel, grads._dt, grads.n, max_norm, grads._out, _ptr(norm),
+            _ptr(ws), ws.numel(), _ptr(dev_err), _stream(dev)), "moe_grad_norm_clip")
+    return norm

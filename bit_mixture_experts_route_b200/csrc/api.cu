@@ -507,3 +507,176 @@ moe_status_t moe_layer_forward(const void* X, const float* logits, int T, int E,
 }
 
 }  // extern "C"
+
+// ---- the dense training-side operators
+
+namespace {
+
+bool half_dtype(moe_dtype_t d) { return d == MOE_DT_BF16 || d == MOE_DT_F16; }
+constexpr int kMaxRows = 1 << 20;  // rows, widths
+constexpr int kMaxVocab = 1 << 24;
+
+moe_status_t ffn_shape(int T, int H, int I) {
+  if (T < 0 || H < 1 || I < 1) return MOE_ERR_INVALID_ARG;
+  if (H % 8 || I % 8 || T > kMaxRows || H > kMaxRows || I > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t ce_shape(int T, int H, int V) {
+  if (T < 0 || H < 1 || V < 1) return MOE_ERR_INVALID_ARG;
+  if (H % 8 || T > kMaxRows || H > kMaxRows || V > kMaxVocab) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// A gradient over no rows: zeros.
+moe_status_t zero16(void* p, size_t n, void* stream) {
+  if (!p) return MOE_OK;
+  return from_cuda(cudaMemsetAsync(p, 0, 2 * n, (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_gated_ffn_forward_workspace_size(int T, int H, int I, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  if (moe_status_t st = ffn_shape(T, H, I)) return st;
+  *bytes = moe_launch::gated_ffn_forward_workspace(T, H, I);
+  return MOE_OK;
+}
+
+moe_status_t moe_gated_ffn_backward_workspace_size(int T, int H, int I, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  if (moe_status_t st = ffn_shape(T, H, I)) return st;
+  *bytes = moe_launch::gated_ffn_backward_workspace(T, H, I);
+  return MOE_OK;
+}
+
+moe_status_t moe_gated_ffn_forward(const void* X, moe_dtype_t dtype, const void* W_gu,
+                                   const void* W_d, int T, int H, int I, const float* residual,
+                                   void* Y, void* gu, void* workspace, size_t workspace_bytes,
+                                   int32_t* dev_err, void* stream) {
+  if (!half_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+  if (moe_status_t st = ffn_shape(T, H, I)) return st;
+  if (!W_gu || !W_d || (T > 0 && (!X || !Y))) return MOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {X, W_gu, W_d, residual, Y, gu, workspace};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return MOE_ERR_MISALIGNED;
+  if (T == 0) return MOE_OK;
+  if (!workspace || workspace_bytes < moe_launch::gated_ffn_forward_workspace(T, H, I))
+    return MOE_ERR_WORKSPACE;
+  if (moe_status_t st = check_device()) return st;
+  return from_cuda(moe_launch::gated_ffn_forward(X, dtype, W_gu, W_d, T, H, I, residual, Y, gu,
+                                                 workspace, dev_err, (cudaStream_t)stream));
+}
+
+moe_status_t moe_gated_ffn_backward(const void* dY, moe_dtype_t dtype, const void* X,
+                                    const void* gu, const void* W_gu, const void* W_d, int T,
+                                    int H, int I, void* dX, void* dW_gu, void* dW_d,
+                                    void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                    void* stream) {
+  if (!half_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+  if (moe_status_t st = ffn_shape(T, H, I)) return st;
+  if (!W_gu || !W_d || (T > 0 && (!dY || !X || !gu))) return MOE_ERR_INVALID_ARG;
+  if (!dX && !dW_gu && !dW_d && T > 0) return MOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {dY, X, gu, W_gu, W_d, dX, dW_gu, dW_d, workspace};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return MOE_ERR_MISALIGNED;
+  if (T > 0 && (!workspace || workspace_bytes < moe_launch::gated_ffn_backward_workspace(T, H, I)))
+    return MOE_ERR_WORKSPACE;
+  if (moe_status_t st = check_device()) return st;
+  if (T == 0) {
+    if (moe_status_t st = zero16(dW_gu, (size_t)2 * I * H, stream)) return st;
+    return zero16(dW_d, (size_t)H * I, stream);
+  }
+  return from_cuda(moe_launch::gated_ffn_backward(dY, dtype, X, gu, W_gu, W_d, T, H, I, dX, dW_gu,
+                                                  dW_d, workspace, dev_err,
+                                                  (cudaStream_t)stream));
+}
+
+moe_status_t moe_linear_ce_forward_workspace_size(int T, int H, int V, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  if (moe_status_t st = ce_shape(T, H, V)) return st;
+  *bytes = T ? moe_launch::linear_ce_workspace(T, H, V, false) : 0;
+  return MOE_OK;
+}
+
+moe_status_t moe_linear_ce_backward_workspace_size(int T, int H, int V, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  if (moe_status_t st = ce_shape(T, H, V)) return st;
+  *bytes = T ? moe_launch::linear_ce_workspace(T, H, V, true) : 0;
+  return MOE_OK;
+}
+
+moe_status_t moe_linear_ce_forward(const void* X, moe_dtype_t dtype, const void* W,
+                                   const int32_t* targets, int T, int H, int V, int ignore_index,
+                                   float* loss, float* lse, void* workspace,
+                                   size_t workspace_bytes, int32_t* dev_err, void* stream) {
+  if (!half_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+  if (moe_status_t st = ce_shape(T, H, V)) return st;
+  if (!W || (T > 0 && (!X || !targets || !loss || !lse))) return MOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {X, W, targets, loss, lse, workspace};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return MOE_ERR_MISALIGNED;
+  if (T == 0) return MOE_OK;
+  if (!workspace || workspace_bytes < moe_launch::linear_ce_workspace(T, H, V, false))
+    return MOE_ERR_WORKSPACE;
+  if (moe_status_t st = check_device()) return st;
+  return from_cuda(moe_launch::linear_ce_forward(X, dtype, W, targets, T, H, V, ignore_index,
+                                                 loss, lse, workspace, dev_err,
+                                                 (cudaStream_t)stream));
+}
+
+moe_status_t moe_linear_ce_backward(const float* dloss, const void* X, moe_dtype_t dtype,
+                                    const void* W, const int32_t* targets, const float* lse, int T,
+                                    int H, int V, int ignore_index, void* dX, void* dW,
+                                    void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                    void* stream) {
+  if (!half_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+  if (moe_status_t st = ce_shape(T, H, V)) return st;
+  if (!W || (T > 0 && (!dloss || !X || !targets || !lse))) return MOE_ERR_INVALID_ARG;
+  if (!dX && !dW && T > 0) return MOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {dloss, X, W, targets, lse, dX, dW, workspace};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return MOE_ERR_MISALIGNED;
+  if (T > 0 && (!workspace || workspace_bytes < moe_launch::linear_ce_workspace(T, H, V, true)))
+    return MOE_ERR_WORKSPACE;
+  if (moe_status_t st = check_device()) return st;
+  if (T == 0) return zero16(dW, (size_t)V * H, stream);
+  return from_cuda(moe_launch::linear_ce_backward(dloss, X, dtype, W, targets, lse, T, H, V,
+                                                  ignore_index, dX, dW, workspace, dev_err,
+                                                  (cudaStream_t)stream));
+}
+
+moe_status_t moe_grad_norm_clip_workspace_size(int n, size_t* bytes) {
+  if (!bytes || n < 0) return MOE_ERR_INVALID_ARG;
+  *bytes = moe_launch::grad_norm_clip_workspace(n);
+  return MOE_OK;
+}
+
+moe_status_t moe_grad_norm_clip(const void* const* grads, const int64_t* numel,
+                                const moe_dtype_t* dtypes, int n, float max_norm,
+                                void* const* outs, float* norm, void* workspace,
+                                size_t workspace_bytes, int32_t* dev_err, void* stream) {
+  if (n < 0 || !norm || !(max_norm >= 0.0f)) return MOE_ERR_INVALID_ARG;
+  if (n > 0 && (!grads || !numel || !dtypes)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return MOE_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(norm) & 3u) return MOE_ERR_MISALIGNED;
+  for (int i = 0; i < n; ++i) {
+    if (!valid_dtype(dtypes[i]) || numel[i] < 0 || numel[i] > (INT64_C(1) << 42))
+      return MOE_ERR_INVALID_ARG;
+    if (numel[i] == 0) continue;
+    const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]);
+    const uintptr_t o = outs ? reinterpret_cast<uintptr_t>(outs[i]) : g;
+    const uintptr_t mask = dtypes[i] == MOE_DT_F32 ? 3u : 1u;
+    if (!g || !o) return MOE_ERR_INVALID_ARG;
+    if ((g | o) & mask) return MOE_ERR_MISALIGNED;
+  }
+  if (!workspace || workspace_bytes < moe_launch::grad_norm_clip_workspace(n))
+    return MOE_ERR_WORKSPACE;
+  if (moe_status_t st = check_device()) return st;
+  return from_cuda(moe_launch::grad_norm_clip(grads, numel, dtypes, n, max_norm, outs, norm,
+                                              workspace, dev_err, (cudaStream_t)stream));
+}
+
+}  // extern "C"

@@ -400,4 +400,30 @@ cudaError_t unpermute_combine(const void* Yp, moe_dtype_t yp_dt,
                               const int32_t* inv_perm, const float* topk_w,
                               int T, int k, int H, void* Y, moe_dtype_t y_dt,
                               cudaStream_t s);
+// Dense gated feed-forward block (ffn.cu); dt F16 or BF16 of every 16-bit
+// matrix.  gu [M, 2I]: written when given (forward), read (backward).  dX,
+// dW_gu, dW_d may be null.
+size_t gated_ffn_forward_workspace(int M, int H, int I);
+size_t gated_ffn_backward_workspace(int M, int H, int I);
+cudaError_t gated_ffn_forward(const void* X, moe_dtype_t dt, const void* W_gu, const void* W_d,
+                              int M, int H, int I, const float* residual, void* Y, void* gu,
+                              void* ws, int32_t* dev_err, cudaStream_t s);
+cudaError_t gated_ffn_backward(const void* dY, moe_dtype_t dt, const void* X, const void* gu,
+                               const void* W_gu, const void* W_d, int M, int H, int I, void* dX,
+                               void* dW_gu, void* dW_d, void* ws, int32_t* dev_err,
+                               cudaStream_t s);
+// Vocabulary cross entropy from hidden rows (linear_ce.cu); dX, dW may be null.
+size_t linear_ce_workspace(int T, int H, int V, bool backward);
+cudaError_t linear_ce_forward(const void* X, moe_dtype_t dt, const void* W, const int32_t* targets,
+                              int T, int H, int V, int ignore_index, float* loss, float* lse,
+                              void* ws, int32_t* dev_err, cudaStream_t s);
+cudaError_t linear_ce_backward(const float* dloss, const void* X, moe_dtype_t dt, const void* W,
+                               const int32_t* targets, const float* lse, int T, int H, int V,
+                               int ignore_index, void* dX, void* dW, void* ws, int32_t* dev_err,
+                               cudaStream_t s);
+// Global gradient norm and clipping (grad_clip.cu); host arrays of n.
+size_t grad_norm_clip_workspace(int n);
+cudaError_t grad_norm_clip(const void* const* grads, const int64_t* numel, const moe_dtype_t* dt,
+                           int n, float max_norm, void* const* outs, float* norm, void* ws,
+                           int32_t* dev_err, cudaStream_t s);
 }  // namespace moe_launch

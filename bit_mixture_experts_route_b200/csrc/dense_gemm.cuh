@@ -1,0 +1,898 @@
+// Dense 16-bit GEMM on the 5th-generation tensor cores, the core of the
+// gated feed-forward block (ffn.cu) and of the vocabulary cross entropy
+// (linear_ce.cu): D[m, n] = sum_k A[m, k] B[n, k], fp32 sums in tensor memory,
+// with the operator's own arithmetic in the epilogue.
+//
+// Either operand may lie the other way round (its m or n index contiguous
+// instead of k): the products of a backward pass read the forward's matrices
+// as they are, through the MN-major forms of the shared-memory descriptor, and
+// nothing is transposed in memory.
+//
+// Work split.  A cluster of two CTAs (two SMs) computes a 256 x 256 tile with
+// tcgen05.mma.cta_group::2: each CTA loads 128 rows of A and 128 rows of B per
+// 64-k stage (32 KB), so a tile reads 64 KB per 256 x 256 x 64 MACs -- half of
+// what two separate 128 x 256 tiles would read -- and each CTA's 128 x 256
+// accumulator block sits in its own tensor memory.  Two accumulators of 256
+// columns fill the 512 columns, so the epilogue of one tile runs under the
+// MMAs of the next.  Persistent: every pair walks units u = pair, pair +
+// pairs, ... of a list of (tile, k split), tiles ordered in groups of GROUP_M
+// row tiles so that the pairs running together share operand tiles in L2.
+//
+// Warp roles (384 threads): warp 0 loads (TMA), warp 1 issues the MMAs (the
+// leader CTA's) and owns the tensor memory, warps 4-11 are the epilogue, two
+// per TMEM lane quarter, each taking 128 of the tile's 256 columns.  16-bit
+// results go through a 128-byte-swizzled staging block per warp (32 rows x 64
+// columns) and leave by TMA, which clips at the matrix's edge; ragged sizes
+// read as zeros.  Every wait is bounded: on expiry MOE_DEVERR_TIMEOUT is set
+// and the kernel drains its copies and MMAs and returns.
+#pragma once
+
+#include "tc_ops.cuh"
+
+namespace moe {
+namespace dense {
+
+using namespace moe::tc;
+
+constexpr int CM = 128;              // rows of A (and of B) per CTA and stage
+constexpr int TILE = 256;            // the pair's tile: 256 x 256
+constexpr int GK = 64;               // k per stage
+constexpr int OPERAND = CM * GK * 2; // 16 KB
+constexpr int STAGE = 2 * OPERAND;   // A then B
+constexpr int EPI_W0 = 4, EPI_NW = 8;
+constexpr int GEMM_THREADS = 32 * (EPI_W0 + EPI_NW);
+constexpr int STG = 32 * 128;        // one staging block: 32 rows x 128 bytes
+constexpr int GROUP_M = 8;
+constexpr int TILE_FLOATS = TILE * TILE;  // a tile of fp32 partial sums, [column][row]
+constexpr float kLog2e = 1.4426950408889634f;
+
+// What the epilogue does with the sums.
+enum Epilogue {
+  E_STORE,       // D0 = 16-bit (sum * *scale + residual)
+  E_PART,        // partial sums to the workspace, [tile][column][row] fp32
+  E_SWIGLU,      // columns are gate [0,128) | up [128,256): D0 = h, D1 = gate | up
+  E_SWIGLU_BWD,  // sums are dh: D0 = h, D1 = dgate | dup, from gu
+  E_STATS,       // per row and 128 columns: max and sum of exponentials; the target's sum
+  E_DLOGITS,     // D0 = (exp(sum - lse) - [column is the target]) * row scale
+};
+constexpr int stages_of(int epi) {
+  return (epi == E_SWIGLU || epi == E_SWIGLU_BWD) ? 4 : (epi == E_PART || epi == E_STATS) ? 6 : 5;
+}
+constexpr int stg_of(int epi) {  // staging blocks per epilogue warp
+  return (epi == E_SWIGLU || epi == E_SWIGLU_BWD) ? 3 : (epi == E_PART || epi == E_STATS) ? 0 : 2;
+}
+
+struct GemmArgs {
+  int N;                 // columns (E_SWIGLU: of h)
+  int m_tiles, n_tiles;  // tiles of 256 rows; of 256 columns (E_SWIGLU: 128)
+  int k_stages;          // ceil(K / 64)
+  int splits, kps;       // k splits and stages per split
+  // *rows (device) replaces the row count (dyn = 1) or the length of the
+  // reduction (dyn = 2); a multiple of 256 rows is readable either way
+  const int* rows;
+  int dyn;
+  float* part;           // E_PART: [split][tile][256][256]
+  int accumulate;        // E_PART: add to what is there
+  const float* residual; // E_STORE: fp32 [rows, N] or null
+  const float* scale;    // E_STORE: device scalar or null
+  int M;
+  const void* gu;        // E_SWIGLU_BWD: [M, 2N] gate | up
+  int save;              // E_SWIGLU: write D1
+  int gate_up;           // E_PART: B and the columns as in E_SWIGLU
+  float2* stats;         // E_STATS: [2 n_tiles][rows_pad]
+  float* target_sum;     // E_STATS: [rows_pad]
+  const int* targets;    // E_STATS, E_DLOGITS: column of each row (relative to this matrix)
+  const float* lse;      // E_DLOGITS
+  const float* row_scale;
+  int col0;              // E_DLOGITS: targets minus col0 are this piece's columns
+  int rows_pad;
+  int32_t* dev_err;
+};
+
+template <int NS, int NSTG>
+struct __align__(8) GemmSmem {
+  uint8_t ab[NS][STAGE];  // 1024-aligned
+  uint8_t stg[EPI_NW][NSTG > 0 ? NSTG : 1][NSTG > 0 ? STG : 16];
+  uint64_t full[NS], empty[NS];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+template <int EPI>
+using GemmSmemFor = GemmSmem<stages_of(EPI), stg_of(EPI)>;
+static_assert(sizeof(GemmSmemFor<E_STORE>) + 1024 <= 227 * 1024, "shared memory budget");
+static_assert(sizeof(GemmSmemFor<E_SWIGLU>) + 1024 <= 227 * 1024, "shared memory budget");
+static_assert(sizeof(GemmSmemFor<E_PART>) + 1024 <= 227 * 1024, "shared memory budget");
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t v);
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map,
+                                                 uint32_t cluster_bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x,
+                                             int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y,
+                                             int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// Shared-memory descriptor of an operand tile.  K-major: 128 rows of 128
+// bytes (64 k), 8-row groups 1024 bytes apart.  MN-major: two blocks of 64
+// rows, each 64 k-lines of 128 bytes (64 rows): 8 k-lines are 1024 bytes (the
+// stride offset), the blocks 8192 bytes (the leading offset).  A k step of 16
+// is 32 bytes further in the first, 16 k-lines = 2048 bytes in the second.
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
+  uint64_t d = sw128_desc(saddr);
+  if (MN) d = (d & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(8192u >> 4) << 16);
+  return d;
+}
+template <bool MN>
+constexpr uint32_t kstep_units() {
+  return (MN ? 2048u : 32u) >> 4;
+}
+
+// Instruction descriptor: D fp32, A and B of T, M = N = 256.
+template <typename T, bool AMN, bool BMN>
+__device__ __forceinline__ constexpr uint32_t gemm_idesc() {
+  const uint32_t f = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+  return (1u << 4) | (f << 7) | (f << 10) | ((AMN ? 1u : 0u) << 15) | ((BMN ? 1u : 0u) << 16) |
+         ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Unit u -> its tile and its k stages [k0, k1).  Tiles run down GROUP_M row
+// tiles before they step to the next column.
+struct Unit {
+  int mt, nt, split, k0, k1;
+};
+__device__ __forceinline__ Unit unit_of(int u, int m_tiles, int n_tiles, int k_stages, int kps) {
+  Unit r;
+  const int tiles = m_tiles * n_tiles;
+  r.split = u / tiles;
+  const int t = u - r.split * tiles;
+  const int per = GROUP_M * n_tiles;
+  const int grp = t / per, first = grp * GROUP_M;
+  const int gm = min(GROUP_M, m_tiles - first);
+  const int in = t - grp * per;
+  r.nt = in / gm;
+  r.mt = first + in - r.nt * gm;
+  r.k0 = min(k_stages, r.split * kps);
+  r.k1 = min(k_stages, r.k0 + kps);
+  return r;
+}
+
+template <typename T, bool AMN, bool BMN, int EPI>
+__global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
+    const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+    const __grid_constant__ CUtensorMap dmap0, const __grid_constant__ CUtensorMap dmap1,
+    const __grid_constant__ GemmArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  constexpr int NS = stages_of(EPI);
+  using Smem = GemmSmemFor<EPI>;
+  Smem& sm = *reinterpret_cast<Smem*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&sm.acc_full[a], 1);
+      mbar_init(&sm.acc_empty[a], EPI_NW * 2);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&sm.tmem_base)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = sm.tmem_base;
+  pdl_wait();
+  pdl_trigger();
+
+  int m_tiles = p.m_tiles, k_stages = p.k_stages, kps = p.kps;
+  if (p.dyn) {
+    const int rows = *p.rows;
+    if (p.dyn == 1) m_tiles = min(m_tiles, (rows + TILE - 1) / TILE);
+    if (p.dyn == 2) {
+      k_stages = min(k_stages, (rows + GK - 1) / GK);
+      kps = max(1, (k_stages + p.splits - 1) / p.splits);
+    }
+  }
+  const int units = m_tiles * p.n_tiles * p.splits;
+  const int u0 = blockIdx.x >> 1, ustep = gridDim.x >> 1;
+  constexpr int NCOLS = EPI == E_SWIGLU ? TILE / 2 : TILE;  // columns of one tile
+  const bool gate_up = EPI == E_SWIGLU || (EPI == E_PART && p.gate_up);
+
+  if (warp == 0) {
+    // ---------------- TMA producer
+    if (lane == 0) {
+      int s = 0, issued = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int u = u0; u < units && ok; u += ustep) {
+        const Unit w = unit_of(u, m_tiles, p.n_tiles, k_stages, kps);
+        const int arow = w.mt * TILE + rank * CM;
+        const int brow = gate_up ? w.nt * CM : w.nt * TILE + rank * CM;
+        for (int k = w.k0; k < w.k1; ++k) {
+          if (!(ok = mbar_wait<true>(&sm.empty[s], ph ^ 1, sm, p.dev_err))) break;
+          if (leader) mbar_arrive_expect_tx(&sm.full[s], 2 * STAGE);
+          const uint32_t bar = cluster_addr(&sm.full[s], 0);
+          uint8_t* a = sm.ab[s];
+          uint8_t* b = a + OPERAND;
+          if (AMN) {
+            tma_load_2d_pair(a, &amap, bar, arow, k * GK);
+            tma_load_2d_pair(a + OPERAND / 2, &amap, bar, arow + 64, k * GK);
+          } else {
+            tma_load_2d_pair(a, &amap, bar, k * GK, arow);
+          }
+          if (gate_up) {  // gate rows in the leader, up rows in its peer
+            tma_load_3d_pair(b, &bmap, bar, k * GK, brow, rank);
+          } else if (BMN) {
+            tma_load_2d_pair(b, &bmap, bar, brow, k * GK);
+            tma_load_2d_pair(b + OPERAND / 2, &bmap, bar, brow + 64, k * GK);
+          } else {
+            tma_load_2d_pair(b, &bmap, bar, k * GK, brow);
+          }
+          ++issued;
+          if (++s == NS) { s = 0; ph ^= 1; }
+        }
+      }
+      // every copy that this pair requested has landed before it may leave
+      // (bounded, and not cut short by an abort)
+      if (leader) {
+        for (int i = 0; i < min(issued, NS); ++i) {
+          if (--s < 0) { s = NS - 1; ph ^= 1; }
+          for (uint32_t n = 0; n < kWaitLimit && !mbar_try_wait_suspend_cl(&sm.full[s], ph); ++n) {
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer
+    if (lane == 0 && leader) {
+      constexpr uint32_t idesc = gemm_idesc<T, AMN, BMN>();
+      const uint64_t ad0 = operand_desc<AMN>(smem_u32(sm.ab[0]));
+      const uint64_t bd0 = operand_desc<BMN>(smem_u32(sm.ab[0]) + OPERAND);
+      int s = 0, lt = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int u = u0; u < units && ok; u += ustep, ++lt) {
+        const Unit w = unit_of(u, m_tiles, p.n_tiles, k_stages, kps);
+        const int acc = lt & 1;
+        if (!(ok = mbar_poll(&sm.acc_empty[acc], ((lt >> 1) & 1) ^ 1, sm, p.dev_err))) break;
+        tc_fence_after();
+        const uint32_t dcol = tmem_base + acc * TILE;
+        for (int k = w.k0; k < w.k1; ++k) {
+          if (!(ok = mbar_poll(&sm.full[s], ph, sm, p.dev_err))) break;
+          tc_fence_after();
+          const uint64_t ad = ad0 + (uint64_t)((s * STAGE) >> 4);
+          const uint64_t bd = bd0 + (uint64_t)((s * STAGE) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < GK / 16; ++kk)
+            mma_ss_pair(dcol, ad + kk * kstep_units<AMN>(), bd + kk * kstep_units<BMN>(), idesc,
+                        (k != w.k0 || kk != 0) ? 1u : 0u);
+          mma_commit_pair(&sm.empty[s]);
+          if (++s == NS) { s = 0; ph ^= 1; }
+        }
+        if (ok) mma_commit_pair(&sm.acc_full[acc]);
+      }
+      // every MMA issued here is done with both CTAs' memory before either leaves
+      mma_commit_pair_local(&sm.drain);
+      for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait_suspend_cl(&sm.drain, 0); ++i) {
+      }
+    }
+  } else if (warp >= EPI_W0) {
+    // ---------------- epilogue: TMEM lanes 32 q .., column half hc
+    const int ew = warp - EPI_W0, q = warp & 3, hc = ew >> 2;
+    const uint32_t lane_addr = (uint32_t)(32 * q) << 16;
+    uint8_t* stg = sm.stg[ew][0];
+    int lt = 0;
+    bool ovf = false;
+    const float scale = (EPI == E_STORE && p.scale) ? *p.scale : 1.0f;
+    // 16 bytes (8 columns) of this lane's row into chunk c of a staging block
+    auto stage16 = [&](int blk, int c, uint4 v) {
+      *reinterpret_cast<uint4*>(stg + blk * STG + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
+    };
+    for (int u = u0; u < units; u += ustep, ++lt) {
+      const Unit w = unit_of(u, m_tiles, p.n_tiles, k_stages, kps);
+      const int acc = lt & 1;
+      const int row = w.mt * TILE + rank * CM + 32 * q + lane;  // this lane's row of D
+      const int row_w = row - lane;                             // the warp's first
+      const bool none = w.k0 >= w.k1;  // nothing to sum: the tensor memory holds old values
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait<true>(&sm.acc_full[acc], (lt >> 1) & 1, sm, p.dev_err)))
+        break;
+      tc_fence_after();
+      const uint32_t tacc = tmem_base + lane_addr + acc * TILE;
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader) mbar_arrive(&sm.acc_empty[acc]);
+          else mbar_arrive_remote(cluster_addr(&sm.acc_empty[acc], 0));
+        }
+      };
+      auto load32 = [&](int col, uint32_t (&v)[32]) {
+        tmem_ld32(tacc + col, v);
+        if (none) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0u;
+        }
+      };
+
+      if constexpr (EPI == E_PART) {
+        const int tile = w.mt * p.n_tiles + w.nt;
+        float* dst = p.part +
+                     ((size_t)w.split * p.m_tiles * p.n_tiles + tile) * (size_t)TILE_FLOATS +
+                     (rank * CM + 32 * q + lane);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const int col = hc * CM + 32 * c;
+          uint32_t v[32];
+          load32(col, v);
+          if (c == 3) release();
+          float* d = dst + (size_t)col * TILE;
+          if (p.accumulate) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              v[i] = __float_as_uint(__uint_as_float(v[i]) + d[(size_t)i * TILE]);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) d[(size_t)i * TILE] = __uint_as_float(v[i]);
+        }
+      } else if constexpr (EPI == E_STATS) {
+        // running maximum m and sum s of exp(l - m) over this half's columns
+        const int tgt = p.targets[row] - w.nt * TILE - hc * CM;
+        float m = -INFINITY, s = 0.0f, tl = 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          load32(hc * CM + 32 * c, v);
+          if (c == 3) release();
+          const int left = p.N - (w.nt * TILE + hc * CM + 32 * c);  // real columns here
+          if (left <= 0) continue;
+          if (left < 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i >= left) v[i] = 0xff800000u;  // -inf
+          }
+          if ((unsigned)(tgt - 32 * c) < 32u) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i == tgt - 32 * c) tl = __uint_as_float(v[i]);
+          }
+          float cm = __uint_as_float(v[0]);
+#pragma unroll
+          for (int i = 1; i < 32; ++i) cm = fmaxf(cm, __uint_as_float(v[i]));
+          const float mn = fmaxf(m, cm);
+          const float mb = mn * kLog2e;
+          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            s0 += exp2_approx(fmaf(__uint_as_float(v[i]), kLog2e, -mb));
+            s1 += exp2_approx(fmaf(__uint_as_float(v[i + 1]), kLog2e, -mb));
+            s2 += exp2_approx(fmaf(__uint_as_float(v[i + 2]), kLog2e, -mb));
+            s3 += exp2_approx(fmaf(__uint_as_float(v[i + 3]), kLog2e, -mb));
+          }
+          s = s * exp2_approx(fmaf(m, kLog2e, -mb)) + ((s0 + s1) + (s2 + s3));
+          m = mn;
+        }
+        p.stats[(size_t)(2 * w.nt + hc) * p.rows_pad + row] = make_float2(m, s);
+        if ((unsigned)tgt < (unsigned)CM) p.target_sum[row] = tl;
+      } else if constexpr (EPI == E_STORE || EPI == E_DLOGITS) {
+        float nlse = 0.f, rs = 0.f;
+        int tgt = -1;
+        if (EPI == E_DLOGITS) {
+          nlse = -p.lse[row] * kLog2e;
+          rs = p.row_scale[row];
+          tgt = p.targets[row] - p.col0 - w.nt * TILE - hc * CM;
+        }
+#pragma unroll 1
+        for (int blk = 0; blk < 2; ++blk) {
+          if (lane == 0) bulk_wait_read<1>();  // this block's last store has left it
+          __syncwarp();
+#pragma unroll
+          for (int h2 = 0; h2 < 2; ++h2) {
+            const int c = 64 * blk + 32 * h2;  // within this warp's 128 columns
+            uint32_t v[32];
+            load32(hc * CM + c, v);
+            if (blk == 1 && h2 == 1) release();
+            if (EPI == E_DLOGITS) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                float pr = exp2_approx(fmaf(__uint_as_float(v[i]), kLog2e, nlse));
+                if (i == tgt - c) pr -= 1.0f;
+                v[i] = __float_as_uint(pr * rs);
+              }
+            } else {
+              if (p.scale) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  v[i] = __float_as_uint(__uint_as_float(v[i]) * scale);
+              }
+              if (p.residual && row < p.M) {
+                const int col = w.nt * TILE + hc * CM + c;
+                const float* r = p.residual + (size_t)row * p.N + col;
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                  if (col + i < p.N) {  // N is a multiple of 8
+                    const float4 x = *reinterpret_cast<const float4*>(r + i);
+                    v[i] = __float_as_uint(__uint_as_float(v[i]) + x.x);
+                    v[i + 1] = __float_as_uint(__uint_as_float(v[i + 1]) + x.y);
+                    v[i + 2] = __float_as_uint(__uint_as_float(v[i + 2]) + x.z);
+                    v[i + 3] = __float_as_uint(__uint_as_float(v[i + 3]) + x.w);
+                  }
+              }
+#pragma unroll
+              for (int i = 0; i < 32; ++i) ovf |= overflows_out<T>(__uint_as_float(v[i]));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint4 o;
+              o.x = pack2<T>(__uint_as_float(v[8 * j]), __uint_as_float(v[8 * j + 1]));
+              o.y = pack2<T>(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3]));
+              o.z = pack2<T>(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5]));
+              o.w = pack2<T>(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7]));
+              stage16(blk, 4 * h2 + j, o);
+            }
+          }
+          fence_proxy_async();
+          __syncwarp();
+          const int col0 = w.nt * TILE + hc * CM + 64 * blk;
+          if (lane == 0 && row_w < (EPI == E_DLOGITS ? p.rows_pad : p.M) && col0 < p.N) {
+            tma_store_2d(&dmap0, stg + blk * STG, col0, row_w);
+            bulk_commit();
+          }
+        }
+      } else {
+        // E_SWIGLU: this warp's 64 gate columns and the same 64 up columns;
+        // E_SWIGLU_BWD: its 128 columns of dh, 64 at a time.
+        // Staging blocks: 0 = h, 1 = gate (gradient), 2 = up (gradient).
+        constexpr int BLKS = EPI == E_SWIGLU ? 1 : 2;
+#pragma unroll 1
+        for (int blk = 0; blk < BLKS; ++blk) {
+          const int c0 = (EPI == E_SWIGLU ? 64 * hc : CM * hc + 64 * blk);  // in the tile
+          const int col0 = w.nt * NCOLS + c0;                               // of h
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int h2 = 0; h2 < 2; ++h2) {
+            uint32_t ho[16], go[16], uo[16];
+            if constexpr (EPI == E_SWIGLU) {
+              uint32_t vg[32], vu[32];
+              load32(c0 + 32 * h2, vg);
+              load32(CM + c0 + 32 * h2, vu);
+              if (h2 == 1) release();
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float g0 = __uint_as_float(vg[i]), g1 = __uint_as_float(vg[i + 1]);
+                const float u0_ = __uint_as_float(vu[i]), u1 = __uint_as_float(vu[i + 1]);
+                // silu by the fast exponential and division: relative error
+                // about 1e-6, far below the 16-bit rounding of h
+                const float h0 = __fdividef(g0, 1.0f + __expf(-g0)) * u0_;
+                const float h1 = __fdividef(g1, 1.0f + __expf(-g1)) * u1;
+                ovf |= overflows_out<T>(h0) | overflows_out<T>(h1);
+                ho[i >> 1] = pack2<T>(h0, h1);
+                go[i >> 1] = pack2<T>(g0, g1);
+                uo[i >> 1] = pack2<T>(u0_, u1);
+                if (p.save)
+                  ovf |= overflows_out<T>(g0) | overflows_out<T>(g1) | overflows_out<T>(u0_) |
+                         overflows_out<T>(u1);
+              }
+            } else {
+              const int col = col0 + 32 * h2;
+              const T* gp = reinterpret_cast<const T*>(p.gu) + (size_t)row * (2 * (size_t)p.N) + col;
+              uint4 gv[4], uv[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const bool in = row < p.M && col + 8 * j < p.N;  // N is a multiple of 8
+                gv[j] = in ? *reinterpret_cast<const uint4*>(gp + 8 * j) : make_uint4(0, 0, 0, 0);
+                uv[j] = in ? *reinterpret_cast<const uint4*>(gp + p.N + 8 * j)
+                           : make_uint4(0, 0, 0, 0);
+              }
+              uint32_t v[32];
+              load32(c0 + 32 * h2, v);
+              if (blk == 1 && h2 == 1) release();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const uint4 g4 = gv[i >> 2], u4 = uv[i >> 2];
+                const uint32_t gw = (i & 3) == 0 ? g4.x : (i & 3) == 1 ? g4.y : (i & 3) == 2 ? g4.z
+                                                                                             : g4.w;
+                const uint32_t uw = (i & 3) == 0 ? u4.x : (i & 3) == 1 ? u4.y : (i & 3) == 2 ? u4.z
+                                                                                             : u4.w;
+                const float2 g = unpack2<T>(gw), uu = unpack2<T>(uw);
+                float dg[2], du[2], hh[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float gg = e ? g.y : g.x, ue = e ? uu.y : uu.x;
+                  const float dh = __uint_as_float(v[2 * i + e]);
+                  const float s = __fdividef(1.0f, 1.0f + __expf(-gg));
+                  const float sg = gg * s;  // silu(g)
+                  hh[e] = sg * ue;
+                  du[e] = dh * sg;
+                  dg[e] = dh * ue * (s + sg * (1.0f - s));
+                  ovf |= overflows_out<T>(du[e]) | overflows_out<T>(dg[e]) |
+                         overflows_out<T>(hh[e]);
+                }
+                ho[i] = pack2<T>(hh[0], hh[1]);
+                go[i] = pack2<T>(dg[0], dg[1]);
+                uo[i] = pack2<T>(du[0], du[1]);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              stage16(0, 4 * h2 + j, make_uint4(ho[4 * j], ho[4 * j + 1], ho[4 * j + 2], ho[4 * j + 3]));
+              if (EPI == E_SWIGLU_BWD || p.save) {
+                stage16(1, 4 * h2 + j,
+                        make_uint4(go[4 * j], go[4 * j + 1], go[4 * j + 2], go[4 * j + 3]));
+                stage16(2, 4 * h2 + j,
+                        make_uint4(uo[4 * j], uo[4 * j + 1], uo[4 * j + 2], uo[4 * j + 3]));
+              }
+            }
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0 && row_w < p.M && col0 < p.N) {
+            tma_store_2d(&dmap0, stg, col0, row_w);
+            if (EPI == E_SWIGLU_BWD || p.save) {
+              tma_store_3d(&dmap1, stg + STG, col0, 0, row_w);
+              tma_store_3d(&dmap1, stg + 2 * STG, col0, 1, row_w);
+            }
+            bulk_commit();
+          }
+        }
+      }
+    }
+    if (stg_of(EPI) > 0 && lane == 0) bulk_wait_all();
+    __syncwarp();
+    // the loop exits are warp-uniform, so every lane takes part
+    if (__any_sync(0xffffffffu, ovf) && lane == 0) set_dev_err(p.dev_err, MOE_DEVERR_RANGE);
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"(512));
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+// Tensor map of a row-major 16-bit matrix [rows, cols] with `ld` elements per
+// row; box of 64 columns x box_rows, 128-byte swizzle.
+template <typename T>
+inline bool map_2d(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld,
+                   int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, es[2] = {1, 1};
+  return encode_tiled_cached(
+             m,
+             std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+             2, const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+template <typename T>
+inline bool map_3d(CUtensorMap* m, const void* p, const int64_t (&d)[3], const int64_t (&ld)[2],
+                   const int (&b)[3]) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d[0], (cuuint64_t)d[1], (cuuint64_t)d[2]};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld[0] * 2, (cuuint64_t)ld[1] * 2};
+  const cuuint32_t box[3] = {(cuuint32_t)b[0], (cuuint32_t)b[1], (cuuint32_t)b[2]},
+                   es[3] = {1, 1, 1};
+  return encode_tiled_cached(
+             m,
+             std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+             3, const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// An operand of the GEMM: rows (m or n) x k, either way round.
+struct Operand {
+  const void* p;
+  int64_t rows, k, ld;  // ld: elements between consecutive lines of memory
+};
+template <typename T, bool MN>
+inline bool operand_map(CUtensorMap* m, const Operand& o) {
+  return MN ? map_2d<T>(m, o.p, o.k, o.rows, o.ld, GK) : map_2d<T>(m, o.p, o.rows, o.k, o.ld, CM);
+}
+
+// Pairs of CTAs that fit on the device at once (one CTA per SM).
+inline int max_pairs(const void* kern, size_t smem) {
+  static std::mutex mu;
+  static std::unordered_map<uint64_t, int> cache;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  const uint64_t key = (reinterpret_cast<uint64_t>(kern) << 6) ^ (uint64_t)dev;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    const auto it = cache.find(key);
+    if (it != cache.end()) return it->second;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * std::max(1, device_sm_count() / 2));
+  cfg.blockDim = dim3(GEMM_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    n = std::max(1, device_sm_count() / 2);
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  cache[key] = n;
+  return n;
+}
+
+template <typename T, bool AMN, bool BMN, int EPI>
+cudaError_t launch_gemm_maps(const CUtensorMap& am, const CUtensorMap& bm, const CUtensorMap& d0,
+                             const CUtensorMap& d1, const GemmArgs& p, cudaStream_t s) {
+  auto kern = dense_gemm_kernel<T, AMN, BMN, EPI>;
+  const void* kp = reinterpret_cast<const void*>(kern);
+  const size_t smem = sizeof(GemmSmemFor<EPI>) + 1024;
+  cudaError_t err = set_max_dynamic_smem_once(kp, (int)smem);
+  if (err != cudaSuccess) return err;
+  const int64_t units = (int64_t)p.m_tiles * p.n_tiles * p.splits;
+  if (units > INT32_MAX / 2) return cudaErrorInvalidValue;
+  const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(max_pairs(kp, smem), units));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(GEMM_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, am, bm, d0, d1, p);
+}
+
+// The GEMM on two plain operands; d0 / d1 are the epilogue's output maps.
+template <typename T, bool AMN, bool BMN, int EPI>
+cudaError_t launch_gemm(const Operand& a, const Operand& b, const CUtensorMap& d0,
+                        const CUtensorMap& d1, const GemmArgs& p, cudaStream_t s) {
+  CUtensorMap am, bm;
+  if (!operand_map<T, AMN>(&am, a) || !operand_map<T, BMN>(&bm, b)) return cudaErrorInvalidValue;
+  return launch_gemm_maps<T, AMN, BMN, EPI>(am, bm, d0, d1, p, s);
+}
+
+inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// Splits of the reduction for a GEMM of `tiles` tiles and k_stages stages, at
+// most `most` (what the workspace holds).  Modelled in units of one stage's
+// MMAs (0.27 us): a pair's rounds of (stages + 6 to fill and drain), and with
+// more than one split the second kernel and the partial sums' way through L2.
+inline int pick_splits(int tiles, int k_stages, int most, bool direct_needs_finish) {
+  const int pairs = std::max(1, device_sm_count() / 2);
+  int best = 1;
+  double best_cost = 1e30;
+  for (int sp = 1; sp <= most && sp <= k_stages; ++sp) {
+    const int kps = ceil_div(k_stages, sp);
+    if (ceil_div(k_stages, kps) != sp) continue;  // an empty last split
+    const double rounds = ceil_div((int64_t)tiles * sp, pairs);
+    double cost = rounds * (kps + 6);
+    if (sp > 1 || direct_needs_finish) cost += 10.0 + 0.2 * tiles * sp / 4.0;
+    if (cost < best_cost) { best_cost = cost; best = sp; }
+  }
+  return best;
+}
+
+// ---------------------------------------------------------------- joining the splits
+
+enum Finish {
+  F_PLAIN,       // out = 16-bit (sum * *scale + residual)
+  F_SWIGLU,      // partial columns gate | up: out = h, out1 = gate | up (if given)
+  F_SWIGLU_BWD,  // sums are dh: out = h, out1 = dgate | dup, from gu
+};
+struct FinishArgs {
+  const float* part;  // [split][tile][256 columns][256 rows]
+  int splits, n_tiles;
+  size_t split_stride;  // floats
+  int M, N;             // rows and columns of out
+  const float* residual;
+  const float* scale;
+  const int* row_of;    // F_PLAIN: out row -> row of the sums, -1 for a zero row; or null
+  const void* gu;
+  void* out;
+  void* out1;
+  int32_t* dev_err;
+};
+
+// One block joins 32 rows x 64 columns: the splits' partial sums are added in
+// split order (so the result does not depend on timing), turned from
+// [column][row] to rows through shared memory, and finished.  Bound by the
+// partial sums' way out of L2.
+template <typename T, int FIN>
+__global__ void __launch_bounds__(256) finish_kernel(FinishArgs p) {
+  __shared__ float t0[64][33];
+  __shared__ float t1[FIN == F_SWIGLU ? 64 : 1][33];
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c0 = blockIdx.x * 64, row0 = blockIdx.y * 32;
+  {
+    const int row = row0 + lane;
+    int cr = row < p.M ? row : -1;
+    if (p.row_of && cr >= 0) cr = p.row_of[row];
+    const int nt = FIN == F_SWIGLU ? c0 / (TILE / 2) : c0 / TILE;
+    const int col = FIN == F_SWIGLU ? c0 % (TILE / 2) : c0 % TILE;
+    const float* src = p.part + ((size_t)(cr >> 8) * p.n_tiles + nt) * (size_t)TILE_FLOATS +
+                       (size_t)col * TILE + (cr & 255);
+    float a[8] = {}, b[8] = {};
+    if (cr >= 0) {
+      for (int sp = 0; sp < p.splits; ++sp, src += p.split_stride) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          a[i] += src[(size_t)(warp + 8 * i) * TILE];
+          if (FIN == F_SWIGLU) b[i] += src[(size_t)(warp + 8 * i + TILE / 2) * TILE];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      t0[warp + 8 * i][lane] = a[i];
+      if (FIN == F_SWIGLU) t1[warp + 8 * i][lane] = b[i];
+    }
+  }
+  __syncthreads();
+  const int r = threadIdx.x >> 3, cj = (threadIdx.x & 7) * 8;
+  const int row = row0 + r, col = c0 + cj;
+  if (row >= p.M || col >= p.N) return;  // N is a multiple of 8
+  float v[8], w[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    v[e] = t0[cj + e][r];
+    w[e] = FIN == F_SWIGLU ? t1[cj + e][r] : 0.0f;
+  }
+  bool ovf = false;
+  auto put = [&](void* base, size_t at, const float (&x)[8]) {
+    uint4 o;
+    o.x = pack2<T>(x[0], x[1]);
+    o.y = pack2<T>(x[2], x[3]);
+    o.z = pack2<T>(x[4], x[5]);
+    o.w = pack2<T>(x[6], x[7]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ovf |= overflows_out<T>(x[e]);
+    *reinterpret_cast<uint4*>(reinterpret_cast<T*>(base) + at) = o;
+  };
+  const size_t at = (size_t)row * p.N + col;
+  const size_t at2 = (size_t)row * (2 * (size_t)p.N) + col;  // in a gate | up row
+  if (FIN == F_PLAIN) {
+    if (p.scale) {
+      const float sc = *p.scale;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= sc;
+    }
+    if (p.residual) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += p.residual[at + e];
+    }
+    put(p.out, at, v);
+  } else if (FIN == F_SWIGLU) {
+    float h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = __fdividef(v[e], 1.0f + __expf(-v[e])) * w[e];
+    put(p.out, at, h);
+    if (p.out1) {
+      put(p.out1, at2, v);
+      put(p.out1, at2 + p.N, w);
+    }
+  } else {
+    const T* gu = reinterpret_cast<const T*>(p.gu);
+    float h[8], dg[8], du[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float g = to_f32<T>(gu[at2 + e]), u = to_f32<T>(gu[at2 + p.N + e]);
+      const float s = __fdividef(1.0f, 1.0f + __expf(-g)), sg = g * s;
+      h[e] = sg * u;
+      du[e] = v[e] * sg;
+      dg[e] = v[e] * u * (s + sg * (1.0f - s));
+    }
+    put(p.out, at, h);
+    put(p.out1, at2, dg);
+    put(p.out1, at2 + p.N, du);
+  }
+  if (ovf) set_dev_err(p.dev_err, MOE_DEVERR_RANGE);
+}
+
+template <typename T, int FIN>
+cudaError_t launch_finish(const FinishArgs& p, cudaStream_t s) {
+  return launch_pdl(finish_kernel<T, FIN>, dim3(ceil_div(p.N, 64), ceil_div(p.M, 32)), dim3(256), 0,
+                    s, p);
+}
+
+}  // namespace dense
+}  // namespace moe

@@ -1,0 +1,281 @@
+// Global 2-norm of many gradient tensors and clipping by it:
+//   norm = sqrt(sum g^2),  c = min(1, max_norm / (norm + 1e-6)),  out = c g.
+// Two launches: every block sums the squares of its share of the elements and
+// leaves one double; every block of the second adds those in the same fixed
+// order (so all agree, and a run repeats bit for bit) and scales its share.
+// The tensors' addresses travel in the launch's parameters, up to kMaxTensors
+// per launch, so a captured graph holds them and no device table is needed.
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxTensors = 512;  // per launch: 24 bytes each of the 32764 of a launch's parameters
+constexpr int kThreads = 512;
+constexpr int kChunk = 8192;      // elements of one piece of work, within one tensor
+constexpr int kMaxBlocks = 148 * 4;
+
+template <int CAP>
+struct Table {
+  const void* in[CAP];
+  void* out[CAP];
+  int chunk0[CAP + 1];  // chunks before tensor i
+  uint32_t tail[CAP];   // elements of its last chunk | dtype << 30
+  int n;
+};
+
+// Squares of eight values added in fp32, unless they leave its range, then in
+// fp64; the running sum is fp64 either way.
+__device__ __forceinline__ void add_squares(double& sum, const float (&v)[8]) {
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s = fmaf(v[i], v[i], s);
+  // below 1e-20 a square may have lost bits as a subnormal; NaN fails both
+  if (s > 1e-20f && s < 1e38f) {
+    sum += (double)s;
+  } else {
+    double d = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d += (double)v[i] * (double)v[i];
+    sum += d;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+template <>
+__device__ __forceinline__ void load8<__half>(const __half* p, float (&v)[8]) {
+  const uint4 r = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 r = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    T t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = from_f32<T>(v[i]);
+    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(t);
+  }
+}
+
+// Elements before the first 16-byte boundary at or after p.
+template <typename T>
+__device__ __forceinline__ int head_of(const T* p, int n) {
+  const int h = (int)(((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(T));
+  return min(h, n);
+}
+
+template <typename T>
+__device__ __forceinline__ double chunk_squares(const T* p, int n) {
+  double sum = 0.0;
+  const int head = head_of(p, n), vecs = (n - head) / 8, tail0 = head + 8 * vecs;
+  for (int i = threadIdx.x; i < vecs; i += kThreads) {
+    float v[8];
+    load8<T>(p + head + 8 * i, v);
+    add_squares(sum, v);
+  }
+  const int rest = head + (n - tail0);  // fewer than 16 elements
+  if ((int)threadIdx.x < rest) {
+    const int i = threadIdx.x < head ? threadIdx.x : tail0 + (threadIdx.x - head);
+    const double d = (double)to_f32<T>(p[i]);
+    sum += d * d;
+  }
+  return sum;
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_scale(const T* p, T* o, int n, float c) {
+  const int head = head_of(o, n);
+  if (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0) {
+    const int vecs = (n - head) / 8, tail0 = head + 8 * vecs;
+    for (int i = threadIdx.x; i < vecs; i += kThreads) {
+      float v[8];
+      load8<T>(p + head + 8 * i, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= c;
+      store8<T>(o + head + 8 * i, v);
+    }
+    const int rest = head + (n - tail0);
+    if ((int)threadIdx.x < rest) {
+      const int i = threadIdx.x < head ? threadIdx.x : tail0 + (threadIdx.x - head);
+      o[i] = from_f32<T>(to_f32<T>(p[i]) * c);
+    }
+  } else {  // the two lie differently against 16 bytes
+    for (int i = threadIdx.x; i < n; i += kThreads) o[i] = from_f32<T>(to_f32<T>(p[i]) * c);
+  }
+}
+
+template <int CAP>
+__device__ __forceinline__ int tensor_of(const Table<CAP>& t, int chunk) {
+  int lo = 0, hi = t.n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t.chunk0[mid] <= chunk) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ double block_sum(double v) {
+  __shared__ double w[kThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) w[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) v += w[i];
+  __syncthreads();
+  return v;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ Table<CAP> t,
+                                                           double* __restrict__ part) {
+  pdl_wait();
+  pdl_trigger();
+  double sum = 0.0;
+  const int chunks = t.chunk0[t.n];
+  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const int i = tensor_of(t, c), k = c - t.chunk0[i];
+    const int n = c + 1 == t.chunk0[i + 1] ? (int)(t.tail[i] & 0x3fffffffu) : kChunk;
+    const size_t at = (size_t)k * kChunk;
+    const uint32_t dt = t.tail[i] >> 30;
+    if (dt == MOE_DT_F32) sum += chunk_squares(static_cast<const float*>(t.in[i]) + at, n);
+    else if (dt == MOE_DT_BF16)
+      sum += chunk_squares(static_cast<const __nv_bfloat16*>(t.in[i]) + at, n);
+    else sum += chunk_squares(static_cast<const __half*>(t.in[i]) + at, n);
+  }
+  sum = block_sum(sum);
+  if (threadIdx.x == 0) part[blockIdx.x] = sum;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table<CAP> t,
+                                                         const double* __restrict__ part,
+                                                         int parts, float max_norm,
+                                                         float* __restrict__ norm_out, int first,
+                                                         int32_t* dev_err) {
+  pdl_wait();
+  pdl_trigger();
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < parts; i += kThreads) sum += part[i];
+  sum = block_sum(sum);
+  const double norm = sqrt(sum);
+  const bool fine = isfinite(norm);
+  const double f = (double)max_norm / (norm + 1e-6);
+  const float c = fine && f < 1.0 ? (float)f : 1.0f;
+  if (first && blockIdx.x == 0 && threadIdx.x == 0) {
+    *norm_out = (float)norm;
+    if (!fine) set_dev_err(dev_err, MOE_DEVERR_NONFINITE);
+  }
+  const int chunks = t.chunk0[t.n];
+  for (int ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
+    const int i = tensor_of(t, ch), k = ch - t.chunk0[i];
+    if (c == 1.0f && t.in[i] == t.out[i]) continue;  // in place and nothing to change
+    const int n = ch + 1 == t.chunk0[i + 1] ? (int)(t.tail[i] & 0x3fffffffu) : kChunk;
+    const size_t at = (size_t)k * kChunk;
+    const uint32_t dt = t.tail[i] >> 30;
+    if (dt == MOE_DT_F32)
+      chunk_scale(static_cast<const float*>(t.in[i]) + at, static_cast<float*>(t.out[i]) + at, n,
+                  c);
+    else if (dt == MOE_DT_BF16)
+      chunk_scale(static_cast<const __nv_bfloat16*>(t.in[i]) + at,
+                  static_cast<__nv_bfloat16*>(t.out[i]) + at, n, c);
+    else
+      chunk_scale(static_cast<const __half*>(t.in[i]) + at, static_cast<__half*>(t.out[i]) + at, n,
+                  c);
+  }
+}
+
+}  // namespace
+}  // namespace moe
+
+namespace moe_launch {
+using namespace moe;
+
+size_t grad_norm_clip_workspace(int n) {
+  const size_t launches = ((size_t)n + kMaxTensors - 1) / kMaxTensors;
+  return std::max<size_t>(launches, 1) * kMaxBlocks * sizeof(double);
+}
+
+// Fills a table with tensors [i0, i1) of the non-empty ones.
+template <int CAP>
+static cudaError_t run(const void* const* grads, const int64_t* numel, const moe_dtype_t* dt, int n,
+                       float max_norm, void* const* outs, float* norm, double* part,
+                       int32_t* dev_err, cudaStream_t s) {
+  struct Launch {
+    int i0, i1, blocks;
+  };
+  const int launches = std::max(1, (n + CAP - 1) / CAP);
+  const int sms = device_sm_count();
+  auto fill = [&](Table<CAP>& t, int l) {
+    t.n = 0;
+    int64_t chunks = 0;
+    t.chunk0[0] = 0;
+    for (int i = l * CAP; i < std::min(n, (l + 1) * CAP); ++i) {
+      if (numel[i] == 0) continue;
+      const int64_t c = (numel[i] + kChunk - 1) / kChunk;
+      t.in[t.n] = grads[i];
+      t.out[t.n] = outs ? outs[i] : const_cast<void*>(grads[i]);
+      t.tail[t.n] = (uint32_t)(numel[i] - (c - 1) * kChunk) | ((uint32_t)dt[i] << 30);
+      chunks += c;
+      t.chunk0[++t.n] = (int)chunks;
+    }
+    return chunks;
+  };
+  auto blocks_of = [&](int64_t chunks) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>(chunks, std::min(4 * sms, kMaxBlocks)));
+  };
+  Table<CAP> t;
+  int parts = 0;
+  for (int l = 0; l < launches; ++l) {
+    const int b = blocks_of(fill(t, l));
+    cudaError_t e = launch_pdl(squares_kernel<CAP>, dim3(b), dim3(kThreads), 0, s, t, part + parts);
+    if (e) return e;
+    parts += b;
+  }
+  for (int l = 0; l < launches; ++l) {
+    const int b = launches > 1 ? blocks_of(fill(t, l)) : parts;
+    cudaError_t e = launch_pdl(scale_kernel<CAP>, dim3(b), dim3(kThreads), 0, s, t,
+                               static_cast<const double*>(part), parts, max_norm, norm,
+                               l == 0 ? 1 : 0, dev_err);
+    if (e) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t grad_norm_clip(const void* const* grads, const int64_t* numel, const moe_dtype_t* dt,
+                           int n, float max_norm, void* const* outs, float* norm, void* ws,
+                           int32_t* dev_err, cudaStream_t s) {
+  double* part = static_cast<double*>(ws);
+  if (n <= 64)
+    return run<64>(grads, numel, dt, n, max_norm, outs, norm, part, dev_err, s);
+  return run<kMaxTensors>(grads, numel, dt, n, max_norm, outs, norm, part, dev_err, s);
+}
+
+}  // namespace moe_launch

@@ -15,7 +15,10 @@
  * Beyond the NF4 forward: the same grouped GEMV on GPTQ-style INT4 and on
  * MXFP4 weights, a per-expert LoRA delta, and the backward steps of the layer
  * with the 4-bit experts frozen (transposed grouped GEMM, SwiGLU, combine and
- * routing backward).
+ * routing backward).  Around the layer, for training: a dense 16-bit gated
+ * feed-forward block, softmax cross entropy over a vocabulary without the
+ * logits (both with their gradients), and the global gradient norm with
+ * clipping.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -557,6 +560,117 @@ moe_status_t moe_layer_forward(const void* X, const float* logits, int T,
                                float* Y, void* workspace,
                                size_t workspace_bytes, int32_t* dev_err,
                                void* stream);
+
+/*
+ * moe_gated_ffn_forward -- dense gated feed-forward block in 16 bits, the
+ * expert that runs beside the routed 4-bit ones (a shared expert, or a model's
+ * dense layers): with W_gu's rows [0, I) gate and [I, 2I) up, as in the fused
+ * expert stacks,
+ *   g = X Wg^T, u = X Wu^T, h = silu(g) * u, Y = h W_d^T (+ residual).
+ *
+ *   dtype     BF16 or F16: the type of X, W_gu, W_d, Y and gu
+ *   X [T, H], W_gu [2I, H], W_d [H, I], Y [T, H]; H % 8 == 0, I % 8 == 0;
+ *             T, H, I <= 2^20 (beyond: MOE_ERR_UNSUPPORTED)
+ *   residual  fp32 [T, H] or NULL, added before the one rounding of Y: e.g. the
+ *             routed experts' Y of moe_layer_forward
+ *   gu        [T, 2I] or NULL: g | u, rounded once, for the backward call
+ *   dev_err   int32 device word or NULL; MOE_DEVERR_RANGE when an F16 h, g, u
+ *             or Y overflowed, MOE_DEVERR_TIMEOUT
+ * Both projections, the activation and the product are one launch (tcgen05);
+ * sums are fp32, h is rounded once to dtype (it is the second product's
+ * operand).  Pointers 16-byte aligned; Y and gu must not overlap the inputs.
+ * T == 0 enqueues nothing.
+ */
+moe_status_t moe_gated_ffn_forward_workspace_size(int T, int H, int I, size_t* bytes);
+moe_status_t moe_gated_ffn_forward(const void* X, moe_dtype_t dtype, const void* W_gu,
+                                   const void* W_d, int T, int H, int I, const float* residual,
+                                   void* Y, void* gu, void* workspace, size_t workspace_bytes,
+                                   int32_t* dev_err, void* stream);
+
+/*
+ * moe_gated_ffn_backward -- its gradients from dY [T, H] and the forward's gu:
+ *   dh = dY W_d, s = sigmoid(g), dg = dh u s (1 + g (1 - s)), du = dh g s,
+ *   dX = [dg | du] W_gu, dW_gu = [dg | du]^T X, dW_d = dY^T h.
+ * (The residual's gradient is dY itself.)
+ *   dX [T, H], dW_gu [2I, H], dW_d [H, I], all of dtype: any may be NULL and is
+ *   then not computed (frozen weights), not all three
+ *   dev_err   RANGE when an F16 value overflowed, TIMEOUT
+ * [dg | du] and h are rounded once to dtype (operands of the products); sums
+ * are fp32 and each gradient is rounded once.  T == 0 zeroes dW_gu and dW_d.
+ */
+moe_status_t moe_gated_ffn_backward_workspace_size(int T, int H, int I, size_t* bytes);
+moe_status_t moe_gated_ffn_backward(const void* dY, moe_dtype_t dtype, const void* X,
+                                    const void* gu, const void* W_gu, const void* W_d, int T,
+                                    int H, int I, void* dX, void* dW_gu, void* dW_d,
+                                    void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                    void* stream);
+
+/*
+ * moe_linear_ce_forward -- softmax cross entropy over a vocabulary, from the
+ * hidden rows and the head's weights; the logits l = X W^T are not kept:
+ *   lse[t] = log sum_v exp(l[t, v]),  loss[t] = lse[t] - l[t, targets[t]]
+ *
+ *   dtype     BF16 or F16: the type of X [T, H] and W [V, H]; H % 8 == 0, any
+ *             V >= 1; T, H <= 2^20, V <= 2^24 (beyond: MOE_ERR_UNSUPPORTED)
+ *   targets   int32 [T]; a row whose target is ignore_index (any value) takes
+ *             no part: its loss and lse are 0, it costs no products, and what
+ *             its X holds (NaN included) reaches nothing.  Any other target
+ *             outside [0, V) sets MOE_DEVERR_BAD_INDEX and is treated the same
+ *   loss, lse fp32 [T]
+ *   dev_err   int32 device word or NULL: BAD_INDEX, TIMEOUT
+ * Sums, maxima and exponentials are fp32.  Pointers 16-byte aligned.
+ */
+moe_status_t moe_linear_ce_forward_workspace_size(int T, int H, int V, size_t* bytes);
+moe_status_t moe_linear_ce_forward(const void* X, moe_dtype_t dtype, const void* W,
+                                   const int32_t* targets, int T, int H, int V, int ignore_index,
+                                   float* loss, float* lse, void* workspace,
+                                   size_t workspace_bytes, int32_t* dev_err, void* stream);
+
+/*
+ * moe_linear_ce_backward -- its gradients for the upstream dloss fp32 [T] (for
+ * a mean over n rows, 1 / n each) and the forward's lse:
+ *   dl[t, v] = (exp(l[t, v] - lse[t]) - [v == targets[t]]) * dloss[t],
+ *   dX = dl W [T, H],  dW = dl^T X [V, H]   (both of dtype; one may be NULL)
+ * The vocabulary is taken in pieces whose dl (16 bits) fits 256 MB of the
+ * workspace; the logits of a piece are computed again.  Ignored rows give zero
+ * rows of dX and nothing to dW.  dl is rounded once to dtype relative to
+ * max |dloss| (the products' operand); sums are fp32, each gradient is rounded
+ * once.  dev_err: BAD_INDEX, RANGE (an F16 gradient overflowed), TIMEOUT.
+ * T == 0 zeroes dW.
+ */
+moe_status_t moe_linear_ce_backward_workspace_size(int T, int H, int V, size_t* bytes);
+moe_status_t moe_linear_ce_backward(const float* dloss, const void* X, moe_dtype_t dtype,
+                                    const void* W, const int32_t* targets, const float* lse, int T,
+                                    int H, int V, int ignore_index, void* dX, void* dW,
+                                    void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                    void* stream);
+
+/*
+ * moe_grad_norm_clip -- the 2-norm of all gradients together, and clipping:
+ *   norm = sqrt(sum over all tensors of g^2)
+ *   outs[i] = g_i * min(1, max_norm / (norm + 1e-6))
+ *
+ *   grads, numel, dtypes, outs: HOST arrays of n; grads[i] a device pointer to
+ *             numel[i] >= 0 contiguous elements of dtypes[i] (F32, BF16, F16),
+ *             aligned to its element size; read during the call only, so a
+ *             captured graph holds the addresses of the capture
+ *   outs      NULL or outs[i] == grads[i]: in place (nothing is written when
+ *             the factor is 1); otherwise a tensor of the same size and type.
+ *             Tensors must not overlap one another
+ *   max_norm  >= 0; INFINITY gives the norm alone
+ *   norm      fp32 [1] (device); a finite norm beyond fp32's range reads as
+ *             infinity, the clipping still uses its fp64 value
+ *   dev_err   MOE_DEVERR_NONFINITE when the norm is not finite (an element is
+ *             NaN or infinite); the factor is then 1
+ * Squares are added in fp32 per eight elements and in fp64 from there, in an
+ * order that depends on the sizes only: the same input gives the same bits.
+ * workspace 16-byte aligned, moe_grad_norm_clip_workspace_size bytes.
+ */
+moe_status_t moe_grad_norm_clip_workspace_size(int n, size_t* bytes);
+moe_status_t moe_grad_norm_clip(const void* const* grads, const int64_t* numel,
+                                const moe_dtype_t* dtypes, int n, float max_norm,
+                                void* const* outs, float* norm, void* workspace,
+                                size_t workspace_bytes, int32_t* dev_err, void* stream);
 
 #ifdef __cplusplus
 }
