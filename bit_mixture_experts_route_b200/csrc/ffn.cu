@@ -10,7 +10,7 @@
 // MMA's operand must be, and the down projection is the second launch.
 // Backward: four launches, the first fusing the whole activation backward
 // (and h again, for dW_d) into the epilogue of dY Wd.
-#include "dense_gemm.cuh"
+#include "ffn_gemv.cuh"
 
 namespace moe {
 namespace {
@@ -80,6 +80,10 @@ cudaError_t forward(const void* X, const void* W_gu, const void* W_d, int M, int
                     const float* residual, void* Y, void* gu, void* ws, int32_t* dev_err,
                     cudaStream_t s) {
   void* h = ws;
+  if (M <= 8)
+    return launch_ffn_gemv<T, 1>(X, W_gu, W_d, M, H, I, residual, Y, gu, h, dev_err, s);
+  if (M <= kGemvRows)
+    return launch_ffn_gemv<T, 2>(X, W_gu, W_d, M, H, I, residual, Y, gu, h, dev_err, s);
   float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + align1k((size_t)M * I * 2));
   const int mt = ceil_div(M, TILE), nt = ceil_div(I, TILE / 2);
   GemmArgs p = {};
@@ -184,6 +188,7 @@ using namespace moe;
 
 size_t gated_ffn_forward_workspace(int M, int H, int I) {
   const int mt = ceil_div(M, TILE);
+  if (M <= kGemvRows) return align1k((size_t)M * I * 2);
   return align1k((size_t)M * I * 2) + std::max(part_bytes(mt * ceil_div(I, TILE / 2), H),
                                                part_bytes(mt * ceil_div(H, TILE), I));
 }
