@@ -10,6 +10,7 @@ shared library is missing, importing any op raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -560,13 +561,24 @@ class _on:
 
 def _matrix(t, shape, name, dtype, device):
     """``t`` is a contiguous tensor of exactly this shape, type and device."""
-    if t is None:
+    if t is None or (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype
+                     and t.shape == shape and t.device == device and t.is_contiguous()):
         return
     _need(t, dtype, name)
     if t.shape != shape:
         raise MoEError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.device != device:
         raise MoEError(f"{name} is on {t.device}, the call's tensors are on {device}")
+
+
+def _raw_stream(device):
+    """The address of ``device``'s current stream; the cheap way where there is one."""
+    if device.type == "cuda" and _current_raw_stream is not None:
+        return _current_raw_stream(device.index)
+    return _stream(device)
+
+
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _dev_word(dev_err, device):
@@ -576,7 +588,9 @@ def _dev_word(dev_err, device):
             raise MoEError(f"dev_err is on {dev_err.device}, the call's tensors are on {device}")
 
 
+@functools.lru_cache(maxsize=1024)
 def _size(fn, *args):
+    """The workspace size that ``fn`` gives: a function of the sizes alone."""
     n = ctypes.c_size_t()
     _check(getattr(load(), fn)(*args, ctypes.byref(n)), fn)
     return n.value
@@ -603,11 +617,13 @@ def _ffn_shapes(X, W_gu, W_d):
     if not isinstance(X, torch.Tensor) or X.dtype not in _HALF:
         raise MoEError("X must be a bf16 or fp16 tensor")
     _need(X, X.dtype, "X", 2)
-    _need(W_d, X.dtype, "W_d", 2)
+    if not isinstance(W_d, torch.Tensor) or W_d.dim() != 2:
+        raise MoEError("W_d must be a tensor of 2 dims")
+    dt, dev = X.dtype, X.device
     T, H = X.shape
     I = W_d.shape[1]
-    _matrix(W_d, (H, I), "W_d", X.dtype, X.device)
-    _matrix(W_gu, (2 * I, H), "W_gu", X.dtype, X.device)
+    _matrix(W_d, (H, I), "W_d", dt, dev)
+    _matrix(W_gu, (2 * I, H), "W_gu", dt, dev)
     return T, H, I
 
 
@@ -632,7 +648,7 @@ def gated_ffn_forward(X, W_gu, W_d, residual=None, save_gu=False, workspace=None
             gu = torch.empty((T, 2 * I), dtype=X.dtype, device=dev)
         _check(load().moe_gated_ffn_forward(
             _ptr(X), DT[X.dtype], _ptr(W_gu), _ptr(W_d), T, H, I, _ptr(residual), _ptr(out),
-            _ptr(gu), _ptr(ws), ws.numel(), _ptr(dev_err), _stream(dev)), "moe_gated_ffn_forward")
+            _ptr(gu), _ptr(ws), ws.numel(), _ptr(dev_err), _raw_stream(dev)), "moe_gated_ffn_forward")
     return out if gu is None else (out, gu)
 
 
@@ -655,7 +671,7 @@ def gated_ffn_backward(dY, X, gu, W_gu, W_d, need_dx=True, need_dw=True, workspa
         dW_d = torch.empty_like(W_d) if need_dw else None
         _check(load().moe_gated_ffn_backward(
             _ptr(dY), DT[X.dtype], _ptr(X), _ptr(gu), _ptr(W_gu), _ptr(W_d), T, H, I, _ptr(dX),
-            _ptr(dW_gu), _ptr(dW_d), _ptr(ws), ws.numel(), _ptr(dev_err), _stream(dev)),
+            _ptr(dW_gu), _ptr(dW_d), _ptr(ws), ws.numel(), _ptr(dev_err), _raw_stream(dev)),
             "moe_gated_ffn_backward")
     return dX, dW_gu, dW_d
 
@@ -672,7 +688,8 @@ def _ce_shapes(X, W, targets):
     if not isinstance(X, torch.Tensor) or X.dtype not in _HALF:
         raise MoEError("X must be a bf16 or fp16 tensor")
     _need(X, X.dtype, "X", 2)
-    _need(W, X.dtype, "W", 2)
+    if not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise MoEError("W must be a tensor of 2 dims")
     T, H = X.shape
     V = W.shape[0]
     _matrix(W, (V, H), "W", X.dtype, X.device)
@@ -694,7 +711,7 @@ def linear_ce_forward(X, W, targets, ignore_index=-100, workspace=None, dev_err=
         lse = torch.empty((T,), dtype=torch.float32, device=dev)
         _check(load().moe_linear_ce_forward(
             _ptr(X), DT[X.dtype], _ptr(W), _ptr(targets), T, H, V, ignore_index, _ptr(loss),
-            _ptr(lse), _ptr(ws), ws.numel(), _ptr(dev_err), _stream(dev)),
+            _ptr(lse), _ptr(ws), ws.numel(), _ptr(dev_err), _raw_stream(dev)),
             "moe_linear_ce_forward")
     return loss, lse
 
@@ -717,7 +734,7 @@ def linear_ce_backward(dloss, X, W, targets, lse, ignore_index=-100, need_dx=Tru
         dW = torch.empty_like(W) if need_dw else None
         _check(load().moe_linear_ce_backward(
             _ptr(dloss), _ptr(X), DT[X.dtype], _ptr(W), _ptr(targets), _ptr(lse), T, H, V,
-            ignore_index, _ptr(dX), _ptr(dW), _ptr(ws), ws.numel(), _ptr(dev_err), _stream(dev)),
+            ignore_index, _ptr(dX), _ptr(dW), _ptr(ws), ws.numel(), _ptr(dev_err), _raw_stream(dev)),
             "moe_linear_ce_backward")
     return dX, dW
 
@@ -774,5 +791,5 @@ def grad_norm_clip(grads, max_norm, norm=None, workspace=None, dev_err=None):
             norm = torch.empty((1,), dtype=torch.float32, device=dev)
         _check(load().moe_grad_norm_clip(
             grads._in, grads._numel, grads._dt, grads.n, max_norm, grads._out, _ptr(norm),
-            _ptr(ws), ws.numel(), _ptr(dev_err), _stream(dev)), "moe_grad_norm_clip")
+            _ptr(ws), ws.numel(), _ptr(dev_err), _raw_stream(dev)), "moe_grad_norm_clip")
     return norm
