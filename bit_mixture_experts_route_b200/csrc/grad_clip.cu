@@ -11,9 +11,15 @@ namespace moe {
 namespace {
 
 constexpr int kMaxTensors = 512;  // per launch: 24 bytes each of the 32764 of a launch's parameters
-constexpr int kThreads = 512;
-constexpr int kChunk = 8192;      // elements of one piece of work, within one tensor
-constexpr int kMaxBlocks = 148 * 4;
+constexpr int kThreads = 256;
+constexpr int kChunkBytes = 32768;  // one piece of work, within one tensor
+// Blocks: the squares' are resident all at once (their number is that of the
+// partial sums); the scaling's are many, which keeps reads and writes mixed.
+constexpr int kSumBlocks = 148 * 6, kScaleBlocks = 148 * 128;
+// elements of a chunk: 16-bit types 16384, fp32 8192
+__host__ __device__ constexpr int chunk_of(uint32_t dt) {
+  return dt == MOE_DT_F32 ? kChunkBytes / 4 : kChunkBytes / 2;
+}
 
 template <int CAP>
 struct Table {
@@ -24,64 +30,67 @@ struct Table {
   int n;
 };
 
-// Squares of eight values added in fp32, unless they leave its range, then in
+// Squares of N values added in fp32, unless they leave its range, then in
 // fp64; the running sum is fp64 either way.
-__device__ __forceinline__ void add_squares(double& sum, const float (&v)[8]) {
+template <int N>
+__device__ __forceinline__ void add_squares(double& sum, const float (&v)[N]) {
   float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s = fmaf(v[i], v[i], s);
+  for (int i = 0; i < N; ++i) s = fmaf(v[i], v[i], s);
   // below 1e-20 a square may have lost bits as a subnormal; NaN fails both
   if (s > 1e-20f && s < 1e38f) {
     sum += (double)s;
   } else {
     double d = 0.0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) d += (double)v[i] * (double)v[i];
+    for (int i = 0; i < N; ++i) d += (double)v[i] * (double)v[i];
     sum += d;
   }
 }
 
+// The values of 16 bytes of T.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+constexpr int per16() {
+  return 16 / (int)sizeof(T);
 }
-template <>
-__device__ __forceinline__ void load8<__half>(const __half* p, float (&v)[8]) {
-  const uint4 r = *reinterpret_cast<const uint4*>(p);
+template <typename T>
+__device__ __forceinline__ void unpack16(uint4 r, float (&v)[per16<T>()]) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 r = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    if constexpr (sizeof(T) == 4) {
+      v[i] = __uint_as_float(w[i]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    } else {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
   }
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    T t[8];
+__device__ __forceinline__ uint4 pack16(const float (&v)[per16<T>()]) {
+  uint4 r;
+  uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = from_f32<T>(v[i]);
-    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(t);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      w[i] = __float_as_uint(v[i]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
   }
+  r.x = w[0]; r.y = w[1]; r.z = w[2]; r.w = w[3];
+  return r;
 }
+
+constexpr int kSumUnroll = 4, kScaleUnroll = 4;  // 16-byte loads in flight per thread
 
 // Elements before the first 16-byte boundary at or after p.
 template <typename T>
@@ -92,12 +101,22 @@ __device__ __forceinline__ int head_of(const T* p, int n) {
 
 template <typename T>
 __device__ __forceinline__ double chunk_squares(const T* p, int n) {
+  constexpr int P = per16<T>();
   double sum = 0.0;
-  const int head = head_of(p, n), vecs = (n - head) / 8, tail0 = head + 8 * vecs;
-  for (int i = threadIdx.x; i < vecs; i += kThreads) {
-    float v[8];
-    load8<T>(p + head + 8 * i, v);
-    add_squares(sum, v);
+  const int head = head_of(p, n), vecs = (n - head) / P, tail0 = head + P * vecs;
+  const uint4* q = reinterpret_cast<const uint4*>(p + head);
+  for (int i0 = threadIdx.x; i0 < vecs; i0 += kSumUnroll * kThreads) {
+    uint4 r[kSumUnroll];
+#pragma unroll
+    for (int j = 0; j < kSumUnroll; ++j)
+      r[j] = i0 + j * kThreads < vecs ? __ldg(q + i0 + j * kThreads) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < kSumUnroll; ++j) {
+      if (i0 + j * kThreads >= vecs) break;
+      float v[P];
+      unpack16<T>(r[j], v);
+      add_squares(sum, v);
+    }
   }
   const int rest = head + (n - tail0);  // fewer than 16 elements
   if ((int)threadIdx.x < rest) {
@@ -112,13 +131,24 @@ template <typename T>
 __device__ __forceinline__ void chunk_scale(const T* p, T* o, int n, float c) {
   const int head = head_of(o, n);
   if (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0) {
-    const int vecs = (n - head) / 8, tail0 = head + 8 * vecs;
-    for (int i = threadIdx.x; i < vecs; i += kThreads) {
-      float v[8];
-      load8<T>(p + head + 8 * i, v);
+    constexpr int P = per16<T>();
+    const int vecs = (n - head) / P, tail0 = head + P * vecs;
+    const uint4* q = reinterpret_cast<const uint4*>(p + head);
+    uint4* w = reinterpret_cast<uint4*>(o + head);
+    for (int i0 = threadIdx.x; i0 < vecs; i0 += kScaleUnroll * kThreads) {
+      uint4 r[kScaleUnroll];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= c;
-      store8<T>(o + head + 8 * i, v);
+      for (int j = 0; j < kScaleUnroll; ++j)
+        if (i0 + j * kThreads < vecs) r[j] = q[i0 + j * kThreads];
+#pragma unroll
+      for (int j = 0; j < kScaleUnroll; ++j) {
+        if (i0 + j * kThreads >= vecs) break;
+        float v[P];
+        unpack16<T>(r[j], v);
+#pragma unroll
+        for (int e = 0; e < P; ++e) v[e] *= c;
+        w[i0 + j * kThreads] = pack16<T>(v);
+      }
     }
     const int rest = head + (n - tail0);
     if ((int)threadIdx.x < rest) {
@@ -154,7 +184,7 @@ __device__ __forceinline__ double block_sum(double v) {
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ Table<CAP> t,
+__global__ void __launch_bounds__(kThreads, 6) squares_kernel(const __grid_constant__ Table<CAP> t,
                                                            double* __restrict__ part) {
   pdl_wait();
   pdl_trigger();
@@ -162,9 +192,9 @@ __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant
   const int chunks = t.chunk0[t.n];
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
     const int i = tensor_of(t, c), k = c - t.chunk0[i];
-    const int n = c + 1 == t.chunk0[i + 1] ? (int)(t.tail[i] & 0x3fffffffu) : kChunk;
-    const size_t at = (size_t)k * kChunk;
     const uint32_t dt = t.tail[i] >> 30;
+    const int n = c + 1 == t.chunk0[i + 1] ? (int)(t.tail[i] & 0x3fffffffu) : chunk_of(dt);
+    const size_t at = (size_t)k * chunk_of(dt);
     if (dt == MOE_DT_F32) sum += chunk_squares(static_cast<const float*>(t.in[i]) + at, n);
     else if (dt == MOE_DT_BF16)
       sum += chunk_squares(static_cast<const __nv_bfloat16*>(t.in[i]) + at, n);
@@ -175,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table<CAP> t,
+__global__ void __launch_bounds__(kThreads, 4) scale_kernel(const __grid_constant__ Table<CAP> t,
                                                          const double* __restrict__ part,
                                                          int parts, float max_norm,
                                                          float* __restrict__ norm_out, int first,
@@ -194,12 +224,13 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
     if (!fine) set_dev_err(dev_err, MOE_DEVERR_NONFINITE);
   }
   const int chunks = t.chunk0[t.n];
-  for (int ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
+  // from the last chunk down: what the first pass read last is still in L2
+  for (int ch = chunks - 1 - (int)blockIdx.x; ch >= 0; ch -= gridDim.x) {
     const int i = tensor_of(t, ch), k = ch - t.chunk0[i];
     if (c == 1.0f && t.in[i] == t.out[i]) continue;  // in place and nothing to change
-    const int n = ch + 1 == t.chunk0[i + 1] ? (int)(t.tail[i] & 0x3fffffffu) : kChunk;
-    const size_t at = (size_t)k * kChunk;
     const uint32_t dt = t.tail[i] >> 30;
+    const int n = ch + 1 == t.chunk0[i + 1] ? (int)(t.tail[i] & 0x3fffffffu) : chunk_of(dt);
+    const size_t at = (size_t)k * chunk_of(dt);
     if (dt == MOE_DT_F32)
       chunk_scale(static_cast<const float*>(t.in[i]) + at, static_cast<float*>(t.out[i]) + at, n,
                   c);
@@ -220,7 +251,7 @@ using namespace moe;
 
 size_t grad_norm_clip_workspace(int n) {
   const size_t launches = ((size_t)n + kMaxTensors - 1) / kMaxTensors;
-  return std::max<size_t>(launches, 1) * kMaxBlocks * sizeof(double);
+  return std::max<size_t>(launches, 1) * kSumBlocks * sizeof(double);
 }
 
 // Fills a table with tensors [i0, i1) of the non-empty ones.
@@ -228,40 +259,38 @@ template <int CAP>
 static cudaError_t run(const void* const* grads, const int64_t* numel, const moe_dtype_t* dt, int n,
                        float max_norm, void* const* outs, float* norm, double* part,
                        int32_t* dev_err, cudaStream_t s) {
-  struct Launch {
-    int i0, i1, blocks;
-  };
   const int launches = std::max(1, (n + CAP - 1) / CAP);
-  const int sms = device_sm_count();
   auto fill = [&](Table<CAP>& t, int l) {
     t.n = 0;
     int64_t chunks = 0;
     t.chunk0[0] = 0;
     for (int i = l * CAP; i < std::min(n, (l + 1) * CAP); ++i) {
       if (numel[i] == 0) continue;
-      const int64_t c = (numel[i] + kChunk - 1) / kChunk;
+      const int64_t per = chunk_of(dt[i]), c = (numel[i] + per - 1) / per;
       t.in[t.n] = grads[i];
       t.out[t.n] = outs ? outs[i] : const_cast<void*>(grads[i]);
-      t.tail[t.n] = (uint32_t)(numel[i] - (c - 1) * kChunk) | ((uint32_t)dt[i] << 30);
+      t.tail[t.n] = (uint32_t)(numel[i] - (c - 1) * per) | ((uint32_t)dt[i] << 30);
       chunks += c;
       t.chunk0[++t.n] = (int)chunks;
     }
     return chunks;
   };
-  auto blocks_of = [&](int64_t chunks) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>(chunks, std::min(4 * sms, kMaxBlocks)));
+  auto blocks_of = [](int64_t chunks, int most) {
+    return dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(chunks, most)));
   };
   Table<CAP> t;
   int parts = 0;
+  int64_t chunks = 0;
   for (int l = 0; l < launches; ++l) {
-    const int b = blocks_of(fill(t, l));
-    cudaError_t e = launch_pdl(squares_kernel<CAP>, dim3(b), dim3(kThreads), 0, s, t, part + parts);
+    chunks = fill(t, l);
+    const dim3 b = blocks_of(chunks, kSumBlocks);
+    cudaError_t e = launch_pdl(squares_kernel<CAP>, b, dim3(kThreads), 0, s, t, part + parts);
     if (e) return e;
-    parts += b;
+    parts += (int)b.x;
   }
   for (int l = 0; l < launches; ++l) {
-    const int b = launches > 1 ? blocks_of(fill(t, l)) : parts;
-    cudaError_t e = launch_pdl(scale_kernel<CAP>, dim3(b), dim3(kThreads), 0, s, t,
+    if (launches > 1) chunks = fill(t, l);
+    cudaError_t e = launch_pdl(scale_kernel<CAP>, blocks_of(chunks, kScaleBlocks), dim3(kThreads), 0, s, t,
                                static_cast<const double*>(part), parts, max_norm, norm,
                                l == 0 ? 1 : 0, dev_err);
     if (e) return e;
