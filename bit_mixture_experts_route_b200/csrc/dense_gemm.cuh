@@ -52,7 +52,7 @@ enum Epilogue {
   E_PART,        // partial sums to the workspace, [tile][column][row] fp32
   E_SWIGLU,      // columns are gate [0,128) | up [128,256): D0 = h, D1 = gate | up
   E_SWIGLU_BWD,  // sums are dh: D0 = h, D1 = dgate | dup, from gu
-  E_STATS,       // per row and 128 columns: max and sum of exponentials; the target's sum
+  E_STATS,       // per row and 128 columns: max and sum of exponentials
   E_DLOGITS,     // D0 = (exp(sum - lse) - [column is the target]) * row scale
 };
 constexpr int stages_of(int epi) {
@@ -80,7 +80,7 @@ struct GemmArgs {
   int save;              // E_SWIGLU: write D1
   int gate_up;           // E_PART: B and the columns as in E_SWIGLU
   float2* stats;         // E_STATS: [2 n_tiles][rows_pad]
-  float* target_sum;     // E_STATS: [rows_pad]
+  const float* target_sum;  // E_STATS, E_DLOGITS: the target column's sum of each row
   const int* targets;    // E_STATS, E_DLOGITS: column of each row (relative to this matrix)
   const float* lse;      // E_DLOGITS
   const float* row_scale;
@@ -418,7 +418,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
       } else if constexpr (EPI == E_STATS) {
         // running maximum m and sum s of exp(l - m) over this half's columns
         const int tgt = p.targets[row] - w.nt * TILE - hc * CM;
-        float m = -INFINITY, s = 0.0f, tl = 0.0f;
+        // (the target's sum is given: see linear_ce.cu)
+        const float tl = p.target_sum[row];
+        float m = -INFINITY, s = 0.0f;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
           if ((unsigned)(tgt - 32 * c) < 32u) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (i == tgt - 32 * c) tl = __uint_as_float(v[i]);
+              if (i == tgt - 32 * c) v[i] = __float_as_uint(tl);
           }
           float cm = __uint_as_float(v[0]);
 #pragma unroll
@@ -453,13 +455,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
           m = mn;
         }
         p.stats[(size_t)(2 * w.nt + hc) * p.rows_pad + row] = make_float2(m, s);
-        if ((unsigned)tgt < (unsigned)CM) p.target_sum[row] = tl;
       } else if constexpr (EPI == E_STORE || EPI == E_DLOGITS) {
-        float nlse = 0.f, rs = 0.f;
+        float nlse = 0.f, rs = 0.f, tl = 0.f;
         int tgt = -1;
         if (EPI == E_DLOGITS) {
           nlse = -p.lse[row] * kLog2e;
           rs = p.row_scale[row];
+          tl = p.target_sum[row];
           tgt = p.targets[row] - p.col0 - w.nt * TILE - hc * CM;
         }
 #pragma unroll 1
@@ -474,11 +476,16 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
             if (blk == 1 && h2 == 1) release();
             if (EPI == E_DLOGITS) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                float pr = exp2_approx(fmaf(__uint_as_float(v[i]), kLog2e, nlse));
-                if (i == tgt - c) pr -= 1.0f;
-                v[i] = __float_as_uint(pr * rs);
+              for (int i = 0; i < 32; ++i)
+                v[i] = __float_as_uint(exp2_approx(fmaf(__uint_as_float(v[i]), kLog2e, nlse)));
+              if ((unsigned)(tgt - c) < 32u) {
+                const float pt = exp2_approx(fmaf(tl, kLog2e, nlse)) - 1.0f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (i == tgt - c) v[i] = __float_as_uint(pt);
               }
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * rs);
             } else {
               if (p.scale) {
 #pragma unroll

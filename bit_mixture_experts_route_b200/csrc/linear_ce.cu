@@ -30,94 +30,147 @@ constexpr int kPartTiles = 148;
 
 struct Meta {
   int rows;         // that count
-  float in_scale;   // dl = (p - onehot) * dloss * in_scale
-  float out_scale;  // 1 / in_scale, rounded once
+  float out_scale;  // of dl's products: max |dloss| / the unit of dl
 };
 
-// One block: the rows that count, in order.  inv[t] = place of row t among
-// them or -1; row_of and target by place; loss and lse of ignored rows are 0.
-__global__ void __launch_bounds__(1024) ce_select_kernel(
-    const int* __restrict__ targets, int T, int V, int ignore_index,
-    const float* __restrict__ dloss, float in_unit, Meta* meta, int* __restrict__ inv,
-    int* __restrict__ row_of, float* __restrict__ loss, float* __restrict__ lse,
+// Gathers the rows that count, in order: place among them = how many before it
+// count.  Every block counts for itself (the targets are few next to X), so
+// one launch does it all.  Slot t of a block is row t: if it counts, one warp
+// copies its X, target and gradient scale to its place and computes its
+// target's logit in fp32; if not, the slot writes a zero row behind the last
+// place, up to the end of that 256-row tile.  inv[t] = place or -1; row_of by
+// place; loss and lse of the other rows are 0.
+//
+// The target's logit is computed here, not taken from the tensor cores' sums:
+// those round toward zero at every step (about 2e-6 relative at 2048 terms),
+// which in loss = lse - l[target] and in p[target] - 1 does not average out.
+// It also stands in for the tile's own sum, so that the loss of a confident
+// row stays the logarithm of a sum >= 1.
+template <typename T>
+__global__ void __launch_bounds__(256) ce_gather_kernel(
+    const uint4* __restrict__ X, const uint4* __restrict__ W, int vecs,
+    const int* __restrict__ targets, int rows_all, int V, int ignore_index, int per_block,
+    const float* __restrict__ dloss, const float* __restrict__ lse_in, float in_unit, Meta* meta,
+    int* __restrict__ inv, int* __restrict__ row_of, uint4* __restrict__ Xc,
+    int* __restrict__ ctarget, float* __restrict__ ctsum, float* __restrict__ clse,
+    float* __restrict__ cscale, float* __restrict__ loss, float* __restrict__ lse,
     int32_t* dev_err) {
-  __shared__ int wcount[32];
-  __shared__ float wmax[32];
+  __shared__ int s_all[8], s_before[8];
+  __shared__ float s_big[8];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int base = 0;
+  const int first = blockIdx.x * per_block;
+  int all = 0, before = 0;
   float big = 0.0f;
   bool bad = false;
-  for (int t0 = 0; t0 < T; t0 += 1024) {
-    const int t = t0 + tid;
-    const int y = t < T ? targets[t] : ignore_index;
-    const bool real = t < T && y != ignore_index;
-    const bool keep = real && y >= 0 && y < V;
+  auto count = [&](int t, int y) {
+    const bool real = y != ignore_index;
+    const bool keep = real && (unsigned)y < (unsigned)V;
     bad |= real && !keep;
-    const unsigned m = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0) wcount[warp] = __popc(m);
-    __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < 32; ++w) {
-      before += w < warp ? wcount[w] : 0;
-      all += wcount[w];
-    }
-    __syncthreads();
-    const int at = base + before + __popc(m & lanemask_lt());
-    if (keep) {
-      row_of[at] = t;
-      if (dloss) big = fmaxf(big, fabsf(dloss[t]));
-    } else if (t < T && loss) {
-      loss[t] = 0.0f;
-      lse[t] = 0.0f;
-    }
-    if (t < T) inv[t] = keep ? at : -1;
-    base += all;
+    all += keep;
+    before += keep && t < first;
+    if (keep && dloss) big = fmaxf(big, fabsf(dloss[t]));
+  };
+  const int quads = rows_all / 4;
+#pragma unroll 4
+  for (int i = tid; i < quads; i += 256) {
+    const int4 y = reinterpret_cast<const int4*>(targets)[i];
+    count(4 * i, y.x);
+    count(4 * i + 1, y.y);
+    count(4 * i + 2, y.z);
+    count(4 * i + 3, y.w);
   }
-  if (bad) set_dev_err(dev_err, MOE_DEVERR_BAD_INDEX);
+  if (4 * quads + tid < rows_all) count(4 * quads + tid, targets[4 * quads + tid]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
   big = warp_max(big);
-  if (lane == 0) wmax[warp] = big;
+  if (lane == 0) {
+    s_all[warp] = all;
+    s_before[warp] = before;
+    s_big[warp] = big;
+  }
   __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < 32; ++w) big = fmaxf(big, wmax[w]);
-    // no scaling by a zero, infinite or subnormal maximum
-    if (!(big >= 1e-30f && big <= 1e30f)) big = 1.0f;
-    meta->rows = base;
-    meta->in_scale = in_unit / big;
+  all = before = 0;
+  big = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    all += s_all[w];
+    before += s_before[w];
+    big = fmaxf(big, s_big[w]);
+  }
+  // no scaling by a zero, infinite or tiny maximum
+  if (!(big >= 1e-30f && big <= 1e30f)) big = 1.0f;
+  if (blockIdx.x == 0 && tid == 0) {
+    meta->rows = all;
     meta->out_scale = big / in_unit;
   }
-}
-
-// One warp per place: the row's X, target and gradient scale; zero rows up to
-// the end of the last 256-row tile.
-__global__ void __launch_bounds__(256) ce_gather_kernel(
-    const uint4* __restrict__ X, int vecs, const int* __restrict__ targets,
-    const float* __restrict__ dloss, const float* __restrict__ lse, const Meta* __restrict__ meta,
-    const int* __restrict__ row_of, uint4* __restrict__ Xc, int* __restrict__ ctarget,
-    float* __restrict__ clse, float* __restrict__ cscale) {
-  pdl_wait();
-  pdl_trigger();
-  const int at = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int rows = meta->rows;
-  if (at >= (rows + TILE - 1) / TILE * TILE) return;
-  const bool real = at < rows;
-  const int t = real ? row_of[at] : 0;
-  const uint4* src = X + (size_t)t * vecs;
-  uint4* dst = Xc + (size_t)at * vecs;
-  for (int i = lane; i < vecs; i += 32) dst[i] = real ? src[i] : make_uint4(0, 0, 0, 0);
-  if (lane == 0) {
-    ctarget[at] = real ? targets[t] : -1;
-    if (dloss) {
-      clse[at] = real ? lse[t] : 0.0f;
-      cscale[at] = real ? dloss[t] * meta->in_scale : 0.0f;
+  if (blockIdx.x == 0 && bad) set_dev_err(dev_err, MOE_DEVERR_BAD_INDEX);
+  const int end = (all + TILE - 1) / TILE * TILE;  // of the zero rows
+  for (int g = 0; g < per_block; g += 32) {  // 32 slots at a time
+    const int t0 = first + g;
+    const int y_l = t0 + lane < rows_all && g + lane < per_block ? targets[t0 + lane] : ignore_index;
+    const unsigned kept = __ballot_sync(
+        0xffffffffu, y_l != ignore_index && (unsigned)y_l < (unsigned)V);
+    for (int j = warp; j < 32 && g + j < per_block; j += 8) {
+      const int t = t0 + j;
+      const int rank = before + __popc(kept & ((1u << j) - 1u));  // rows that count before t
+      const bool keep = (kept >> j) & 1u;
+      const int y = __shfl_sync(0xffffffffu, y_l, j);
+      const int at = keep ? rank : all + (t - rank);
+      if (!keep && t < rows_all && lane == 0) {
+        inv[t] = -1;
+        if (loss) {
+          loss[t] = 0.0f;
+          lse[t] = 0.0f;
+        }
+      }
+      if (!keep && at >= end) continue;
+      uint4* dst = Xc + (size_t)at * vecs;
+      float dot = 0.0f;
+      if (keep) {
+        const uint4* src = X + (size_t)t * vecs;
+        const uint4* wr = W + (size_t)y * vecs;
+        float d[4] = {};
+#pragma unroll 4
+        for (int i = lane; i < vecs; i += 32) {
+          const uint4 x = src[i], w = wr[i];
+          dst[i] = x;
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = unpack2<T>(xs[e]), b = unpack2<T>(ws[e]);
+            d[e] = fmaf(a.x, b.x, d[e]);
+            d[e] = fmaf(a.y, b.y, d[e]);
+          }
+        }
+        dot = warp_sum((d[0] + d[1]) + (d[2] + d[3]));
+      } else {
+        for (int i = lane; i < vecs; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
+      }
+      if (lane == 0) {
+        ctarget[at] = keep ? y : -1;
+        ctsum[at] = dot;
+        if (keep) {
+          inv[t] = at;
+          row_of[at] = t;
+        }
+        if (dloss) {
+          clse[at] = keep ? lse_in[t] : 0.0f;
+          cscale[at] = keep ? dloss[t] / big * in_unit : 0.0f;
+        }
+      }
     }
+    before += __popc(kept);
   }
 }
 
 // The (max, sum) pieces of 32 rows: warp w joins pieces w, w + W, ..., then the
 // first warp joins the warps in order.
-constexpr int kJoinWarps = 16;
+constexpr int kJoinWarps = 32;
 __global__ void __launch_bounds__(32 * kJoinWarps) ce_join_kernel(
     const float2* __restrict__ stats, int pieces, int rows_pad, const float* __restrict__ tsum,
     const Meta* __restrict__ meta, const int* __restrict__ row_of, float* __restrict__ loss,
@@ -137,14 +190,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ce_join_kernel(
   };
   if (at < rows) {
     int i = warp;
-    for (; i + 3 * kJoinWarps < pieces; i += 4 * kJoinWarps) {
-      float2 o[4];
+    for (; i < pieces; i += 8 * kJoinWarps) {
+      float2 o[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = stats[(size_t)(i + j * kJoinWarps) * rows_pad + at];
+      for (int j = 0; j < 8; ++j)
+        o[j] = i + j * kJoinWarps < pieces ? stats[(size_t)(i + j * kJoinWarps) * rows_pad + at]
+                                           : make_float2(-INFINITY, 0.0f);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) join(o[j]);
+      for (int j = 0; j < 8; ++j) join(o[j]);
     }
-    for (; i < pieces; i += kJoinWarps) join(stats[(size_t)i * rows_pad + at]);
   }
   part[warp][lane] = make_float2(m, s);
   __syncthreads();
@@ -179,10 +233,10 @@ Space space_of(int T, int H, int V, bool backward) {
   w.inv = take((size_t)T * 4);
   w.row_of = take((size_t)T * 4);
   w.ctarget = take((size_t)w.rows_pad * 4);
+  w.tsum = take((size_t)w.rows_pad * 4);
   w.xc = take((size_t)w.rows_pad * H * 2);
   if (!backward) {
     w.stats = take((size_t)2 * ceil_div(V, TILE) * w.rows_pad * sizeof(float2));
-    w.tsum = take((size_t)w.rows_pad * 4);
   } else {
     w.clse = take((size_t)w.rows_pad * 4);
     w.cscale = take((size_t)w.rows_pad * 4);
@@ -202,22 +256,22 @@ Space space_of(int T, int H, int V, bool backward) {
 }
 
 template <typename T>
-cudaError_t select(const Space& w, char* ws, const void* X, const int* targets, int rows, int H,
-                   int V, int ignore_index, const float* dloss, const float* lse_in, float* loss,
-                   float* lse, int32_t* dev_err, cudaStream_t s) {
+cudaError_t gather(const Space& w, char* ws, const void* X, const void* W, const int* targets,
+                   int rows, int H, int V, int ignore_index, const float* dloss,
+                   const float* lse_in, float* loss, float* lse, int32_t* dev_err,
+                   cudaStream_t s) {
   const float unit = std::is_same<T, __half>::value ? 32768.0f : 1.0f;
-  Meta* meta = reinterpret_cast<Meta*>(ws + w.meta);
-  int* row_of = reinterpret_cast<int*>(ws + w.row_of);
-  cudaError_t e = launch_pdl(ce_select_kernel, dim3(1), dim3(1024), 0, s, targets, rows, V,
-                             ignore_index, dloss, unit, meta, reinterpret_cast<int*>(ws + w.inv),
-                             row_of, loss, lse, dev_err);
-  if (e) return e;
-  return launch_pdl(ce_gather_kernel, dim3(w.rows_pad / 8), dim3(256), 0, s,
-                    static_cast<const uint4*>(X), H / 8, targets, dloss, lse_in,
-                    static_cast<const Meta*>(meta), static_cast<const int*>(row_of),
-                    reinterpret_cast<uint4*>(ws + w.xc), reinterpret_cast<int*>(ws + w.ctarget),
+  // rows per block: each block reads all targets, so more of them per block
+  // once the targets are many
+  const int per = rows <= 8192 ? 8 : 64;
+  return launch_pdl(ce_gather_kernel<T>, dim3(w.rows_pad / per), dim3(256), 0, s,
+                    static_cast<const uint4*>(X), static_cast<const uint4*>(W), H / 8, targets,
+                    rows, V, ignore_index, per, dloss, lse_in, unit,
+                    reinterpret_cast<Meta*>(ws + w.meta), reinterpret_cast<int*>(ws + w.inv),
+                    reinterpret_cast<int*>(ws + w.row_of), reinterpret_cast<uint4*>(ws + w.xc),
+                    reinterpret_cast<int*>(ws + w.ctarget), reinterpret_cast<float*>(ws + w.tsum),
                     reinterpret_cast<float*>(ws + w.clse),
-                    reinterpret_cast<float*>(ws + w.cscale));
+                    reinterpret_cast<float*>(ws + w.cscale), loss, lse, dev_err);
 }
 
 template <typename T>
@@ -225,8 +279,8 @@ cudaError_t forward(const void* X, const void* W, const int* targets, int rows, 
                     int ignore_index, float* loss, float* lse, char* ws, int32_t* dev_err,
                     cudaStream_t s) {
   const Space w = space_of(rows, H, V, false);
-  cudaError_t e = select<T>(w, ws, X, targets, rows, H, V, ignore_index, nullptr, nullptr, loss,
-                            lse, dev_err, s);
+  cudaError_t e = gather<T>(w, ws, X, W, targets, rows, H, V, ignore_index, nullptr, nullptr,
+                            loss, lse, dev_err, s);
   if (e) return e;
   const Meta* meta = reinterpret_cast<const Meta*>(ws + w.meta);
   GemmArgs p = {};
@@ -239,7 +293,7 @@ cudaError_t forward(const void* X, const void* W, const int* targets, int rows, 
   p.rows = &meta->rows;
   p.dyn = 1;
   p.stats = reinterpret_cast<float2*>(ws + w.stats);
-  p.target_sum = reinterpret_cast<float*>(ws + w.tsum);
+  p.target_sum = reinterpret_cast<const float*>(ws + w.tsum);
   p.targets = reinterpret_cast<const int*>(ws + w.ctarget);
   p.rows_pad = w.rows_pad;
   p.dev_err = dev_err;
@@ -250,7 +304,7 @@ cudaError_t forward(const void* X, const void* W, const int* targets, int rows, 
   if (e) return e;
   return launch_pdl(ce_join_kernel, dim3(w.rows_pad / 32), dim3(32 * kJoinWarps), 0, s,
                     static_cast<const float2*>(p.stats), 2 * p.n_tiles, w.rows_pad,
-                    static_cast<const float*>(p.target_sum), meta,
+                    p.target_sum, meta,
                     reinterpret_cast<const int*>(ws + w.row_of), loss, lse);
 }
 
@@ -259,7 +313,7 @@ cudaError_t backward(const float* dloss, const void* X, const void* W, const int
                      const float* lse, int rows, int H, int V, int ignore_index, void* dX,
                      void* dW, char* ws, int32_t* dev_err, cudaStream_t s) {
   const Space w = space_of(rows, H, V, true);
-  cudaError_t e = select<T>(w, ws, X, targets, rows, H, V, ignore_index, dloss, lse, nullptr,
+  cudaError_t e = gather<T>(w, ws, X, W, targets, rows, H, V, ignore_index, dloss, lse, nullptr,
                             nullptr, dev_err, s);
   if (e) return e;
   const Meta* meta = reinterpret_cast<const Meta*>(ws + w.meta);
@@ -282,6 +336,7 @@ cudaError_t backward(const float* dloss, const void* X, const void* W, const int
     p.targets = reinterpret_cast<const int*>(ws + w.ctarget);
     p.lse = reinterpret_cast<const float*>(ws + w.clse);
     p.row_scale = reinterpret_cast<const float*>(ws + w.cscale);
+    p.target_sum = reinterpret_cast<const float*>(ws + w.tsum);
     p.col0 = v0;
     p.rows_pad = w.rows_pad;
     p.dev_err = dev_err;
