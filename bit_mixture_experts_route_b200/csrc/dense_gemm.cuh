@@ -35,10 +35,10 @@ namespace dense {
 using namespace moe::tc;
 
 constexpr int CM = 128;              // rows of A (and of B) per CTA and stage
-constexpr int TILE = 256;            // the pair's tile: 256 x 256
+constexpr int TILE = 256;            // rows of the pair's tile; its columns TN: 256 or 128
 constexpr int GK = 64;               // k per stage
-constexpr int OPERAND = CM * GK * 2; // 16 KB
-constexpr int STAGE = 2 * OPERAND;   // A then B
+constexpr int OPERAND = CM * GK * 2; // 16 KB of A
+constexpr int stage_bytes(int tn) { return OPERAND + tn / 2 * GK * 2; }  // A then B, per CTA
 constexpr int EPI_W0 = 4, EPI_NW = 8;
 constexpr int GEMM_THREADS = 32 * (EPI_W0 + EPI_NW);
 constexpr int STG = 32 * 128;        // one staging block: 32 rows x 128 bytes
@@ -55,11 +55,21 @@ enum Epilogue {
   E_STATS,       // per row and 128 columns: max and sum of exponentials
   E_DLOGITS,     // D0 = (exp(sum - lse) - [column is the target]) * row scale
 };
-constexpr int stages_of(int epi) {
-  return (epi == E_SWIGLU || epi == E_SWIGLU_BWD) ? 4 : (epi == E_PART || epi == E_STATS) ? 6 : 5;
+constexpr bool is_swiglu(int epi) { return epi == E_SWIGLU || epi == E_SWIGLU_BWD; }
+// Epilogue warps per TMEM lane quarter, each with 128 or 64 columns (E_SWIGLU:
+// gate columns and as many up columns).
+constexpr int halves_of(int epi, int tn) {
+  return epi == E_SWIGLU ? tn / 128 : 2;
 }
 constexpr int stg_of(int epi) {  // staging blocks per epilogue warp
-  return (epi == E_SWIGLU || epi == E_SWIGLU_BWD) ? 3 : (epi == E_PART || epi == E_STATS) ? 0 : 2;
+  return is_swiglu(epi) ? 3 : (epi == E_PART || epi == E_STATS) ? 0 : 2;
+}
+constexpr int stg_bytes(int epi, int tn) { return 4 * halves_of(epi, tn) * stg_of(epi) * STG; }
+// As many stages as the shared memory holds beside the staging blocks.
+constexpr int kSmemBudget = 227 * 1024 - 1024 - 512;
+constexpr int stages_of(int epi, int tn) {
+  const int n = (kSmemBudget - stg_bytes(epi, tn)) / stage_bytes(tn);
+  return n > 10 ? 10 : n;
 }
 
 struct GemmArgs {
@@ -67,6 +77,8 @@ struct GemmArgs {
   int m_tiles, n_tiles;  // tiles of 256 rows; of 256 columns (E_SWIGLU: 128)
   int k_stages;          // ceil(K / 64)
   int splits, kps;       // k splits and stages per split
+  int most_splits;       // > 0: the kernel picks the splits itself, at most so many, for
+  int pairs;             // so many pairs (E_PART)
   // *rows (device) replaces the row count (dyn = 1) or the length of the
   // reduction (dyn = 2); a multiple of 256 rows is readable either way
   const int* rows;
@@ -89,21 +101,23 @@ struct GemmArgs {
   int32_t* dev_err;
 };
 
-template <int NS, int NSTG>
+template <int NS, int SB, int NW, int NSTG>
 struct __align__(8) GemmSmem {
-  uint8_t ab[NS][STAGE];  // 1024-aligned
-  uint8_t stg[EPI_NW][NSTG > 0 ? NSTG : 1][NSTG > 0 ? STG : 16];
+  uint8_t ab[NS][SB];  // 1024-aligned
+  uint8_t stg[NW][NSTG > 0 ? NSTG : 1][NSTG > 0 ? STG : 16];
   uint64_t full[NS], empty[NS];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
 };
-template <int EPI>
-using GemmSmemFor = GemmSmem<stages_of(EPI), stg_of(EPI)>;
-static_assert(sizeof(GemmSmemFor<E_STORE>) + 1024 <= 227 * 1024, "shared memory budget");
-static_assert(sizeof(GemmSmemFor<E_SWIGLU>) + 1024 <= 227 * 1024, "shared memory budget");
-static_assert(sizeof(GemmSmemFor<E_PART>) + 1024 <= 227 * 1024, "shared memory budget");
+template <int EPI, int TN>
+using GemmSmemFor =
+    GemmSmem<stages_of(EPI, TN), stage_bytes(TN), 4 * halves_of(EPI, TN), stg_of(EPI)>;
+static_assert(sizeof(GemmSmemFor<E_STORE, 256>) + 1024 <= 227 * 1024, "shared memory budget");
+static_assert(sizeof(GemmSmemFor<E_STORE, 128>) + 1024 <= 227 * 1024, "shared memory budget");
+static_assert(sizeof(GemmSmemFor<E_SWIGLU, 256>) + 1024 <= 227 * 1024, "shared memory budget");
+static_assert(sizeof(GemmSmemFor<E_PART, 256>) + 1024 <= 227 * 1024, "shared memory budget");
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b);
@@ -184,12 +198,12 @@ constexpr uint32_t kstep_units() {
   return (MN ? 2048u : 32u) >> 4;
 }
 
-// Instruction descriptor: D fp32, A and B of T, M = N = 256.
-template <typename T, bool AMN, bool BMN>
+// Instruction descriptor: D fp32, A and B of T, M = 256, N = TN.
+template <typename T, bool AMN, bool BMN, int TN>
 __device__ __forceinline__ constexpr uint32_t gemm_idesc() {
   const uint32_t f = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
   return (1u << 4) | (f << 7) | (f << 10) | ((AMN ? 1u : 0u) << 15) | ((BMN ? 1u : 0u) << 16) |
-         ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
+         ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
 }
 
 __device__ __forceinline__ void mma_ss_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
@@ -223,14 +237,34 @@ __device__ __forceinline__ Unit unit_of(int u, int m_tiles, int n_tiles, int k_s
   return r;
 }
 
-template <typename T, bool AMN, bool BMN, int EPI>
+// Splits of the reduction for `tiles` tiles of `k_stages` stages on `pairs`
+// pairs, at most `most`: the rounds of units (whole tiles or parts of them)
+// that the busiest pair runs, each its stages and about 6 more to fill and
+// drain.
+__host__ __device__ inline int even_splits(int tiles, int k_stages, int most, int pairs) {
+  int best = 1, best_cost = 1 << 30;
+  for (int sp = 1; sp <= most && sp <= k_stages; ++sp) {
+    const int kps = (k_stages + sp - 1) / sp;
+    if ((k_stages + kps - 1) / kps != sp) continue;  // an empty last split
+    const int cost = (tiles * sp + pairs - 1) / pairs * (kps + 6);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = sp;
+    }
+  }
+  return best;
+}
+
+template <typename T, bool AMN, bool BMN, int EPI, int TN>
 __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
     const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
     const __grid_constant__ CUtensorMap dmap0, const __grid_constant__ CUtensorMap dmap1,
     const __grid_constant__ GemmArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  constexpr int NS = stages_of(EPI);
-  using Smem = GemmSmemFor<EPI>;
+  static_assert(EPI != E_PART || TN == TILE, "partial sums are whole 256 x 256 tiles");
+  constexpr int NS = stages_of(EPI, TN), STAGE = stage_bytes(TN), BROWS = TN / 2;
+  constexpr int HALVES = halves_of(EPI, TN);
+  using Smem = GemmSmemFor<EPI, TN>;
   Smem& sm = *reinterpret_cast<Smem*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -244,7 +278,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&sm.acc_full[a], 1);
-      mbar_init(&sm.acc_empty[a], EPI_NW * 2);
+      mbar_init(&sm.acc_empty[a], 4 * HALVES * 2);
     }
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -253,7 +287,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&sm.tmem_base)),
-                 "r"(512));
+                 "r"(2 * TN));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
   tc_fence_before();
@@ -264,7 +298,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
   pdl_wait();
   pdl_trigger();
 
-  int m_tiles = p.m_tiles, k_stages = p.k_stages, kps = p.kps;
+  int m_tiles = p.m_tiles, k_stages = p.k_stages, kps = p.kps, splits = p.splits;
   if (p.dyn) {
     const int rows = *p.rows;
     if (p.dyn == 1) m_tiles = min(m_tiles, (rows + TILE - 1) / TILE);
@@ -273,9 +307,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
       kps = max(1, (k_stages + p.splits - 1) / p.splits);
     }
   }
-  const int units = m_tiles * p.n_tiles * p.splits;
   const int u0 = blockIdx.x >> 1, ustep = gridDim.x >> 1;
-  constexpr int NCOLS = EPI == E_SWIGLU ? TILE / 2 : TILE;  // columns of one tile
+  if (EPI == E_PART && p.most_splits) {
+    splits = even_splits(m_tiles * p.n_tiles, k_stages, p.most_splits, p.pairs);
+    kps = (k_stages + splits - 1) / splits;
+  }
+  const int units = m_tiles * p.n_tiles * splits;
+  constexpr int NCOLS = EPI == E_SWIGLU ? TN / 2 : TN;  // columns of one tile
   const bool gate_up = EPI == E_SWIGLU || (EPI == E_PART && p.gate_up);
 
   if (warp == 0) {
@@ -287,7 +325,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
       for (int u = u0; u < units && ok; u += ustep) {
         const Unit w = unit_of(u, m_tiles, p.n_tiles, k_stages, kps);
         const int arow = w.mt * TILE + rank * CM;
-        const int brow = gate_up ? w.nt * CM : w.nt * TILE + rank * CM;
+        const int brow = gate_up ? w.nt * BROWS : w.nt * TN + rank * BROWS;
         for (int k = w.k0; k < w.k1; ++k) {
           if (!(ok = mbar_wait<true>(&sm.empty[s], ph ^ 1, sm, p.dev_err))) break;
           if (leader) mbar_arrive_expect_tx(&sm.full[s], 2 * STAGE);
@@ -304,7 +342,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
             tma_load_3d_pair(b, &bmap, bar, k * GK, brow, rank);
           } else if (BMN) {
             tma_load_2d_pair(b, &bmap, bar, brow, k * GK);
-            tma_load_2d_pair(b + OPERAND / 2, &bmap, bar, brow + 64, k * GK);
+            if (BROWS > 64) tma_load_2d_pair(b + OPERAND / 2, &bmap, bar, brow + 64, k * GK);
           } else {
             tma_load_2d_pair(b, &bmap, bar, k * GK, brow);
           }
@@ -325,7 +363,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
   } else if (warp == 1) {
     // ---------------- MMA issuer
     if (lane == 0 && leader) {
-      constexpr uint32_t idesc = gemm_idesc<T, AMN, BMN>();
+      constexpr uint32_t idesc = gemm_idesc<T, AMN, BMN, TN>();
       const uint64_t ad0 = operand_desc<AMN>(smem_u32(sm.ab[0]));
       const uint64_t bd0 = operand_desc<BMN>(smem_u32(sm.ab[0]) + OPERAND);
       int s = 0, lt = 0;
@@ -336,7 +374,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
         const int acc = lt & 1;
         if (!(ok = mbar_poll(&sm.acc_empty[acc], ((lt >> 1) & 1) ^ 1, sm, p.dev_err))) break;
         tc_fence_after();
-        const uint32_t dcol = tmem_base + acc * TILE;
+        const uint32_t dcol = tmem_base + acc * TN;
         for (int k = w.k0; k < w.k1; ++k) {
           if (!(ok = mbar_poll(&sm.full[s], ph, sm, p.dev_err))) break;
           tc_fence_after();
@@ -356,12 +394,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
       for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait_suspend_cl(&sm.drain, 0); ++i) {
       }
     }
-  } else if (warp >= EPI_W0) {
-    // ---------------- epilogue: TMEM lanes 32 q .., column half hc
+  } else if (warp >= EPI_W0 && warp < EPI_W0 + 4 * HALVES) {
+    // ---------------- epilogue: TMEM lanes 32 q .., columns CW hc .. of the tile
+    constexpr int CW = NCOLS / HALVES;
     const int ew = warp - EPI_W0, q = warp & 3, hc = ew >> 2;
     const uint32_t lane_addr = (uint32_t)(32 * q) << 16;
     uint8_t* stg = sm.stg[ew][0];
-    int lt = 0;
+    int lt = 0, sb = 0;
     bool ovf = false;
     const float scale = (EPI == E_STORE && p.scale) ? *p.scale : 1.0f;
     // 16 bytes (8 columns) of this lane's row into chunk c of a staging block
@@ -378,7 +417,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
                       mbar_wait<true>(&sm.acc_full[acc], (lt >> 1) & 1, sm, p.dev_err)))
         break;
       tc_fence_after();
-      const uint32_t tacc = tmem_base + lane_addr + acc * TILE;
+      const uint32_t tacc = tmem_base + lane_addr + acc * TN;
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
@@ -416,17 +455,17 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
           for (int i = 0; i < 32; ++i) d[(size_t)i * TILE] = __uint_as_float(v[i]);
         }
       } else if constexpr (EPI == E_STATS) {
-        // running maximum m and sum s of exp(l - m) over this half's columns
-        const int tgt = p.targets[row] - w.nt * TILE - hc * CM;
+        // running maximum m and sum s of exp(l - m) over this warp's columns
+        const int tgt = p.targets[row] - w.nt * TN - hc * CW;
         // (the target's sum is given: see linear_ce.cu)
         const float tl = p.target_sum[row];
         float m = -INFINITY, s = 0.0f;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < CW / 32; ++c) {
           uint32_t v[32];
-          load32(hc * CM + 32 * c, v);
-          if (c == 3) release();
-          const int left = p.N - (w.nt * TILE + hc * CM + 32 * c);  // real columns here
+          load32(hc * CW + 32 * c, v);
+          if (c == CW / 32 - 1) release();
+          const int left = p.N - (w.nt * TN + hc * CW + 32 * c);  // real columns here
           if (left <= 0) continue;
           if (left < 32) {
 #pragma unroll
@@ -454,7 +493,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
           s = s * exp2_approx(fmaf(m, kLog2e, -mb)) + ((s0 + s1) + (s2 + s3));
           m = mn;
         }
-        p.stats[(size_t)(2 * w.nt + hc) * p.rows_pad + row] = make_float2(m, s);
+        p.stats[(size_t)(HALVES * w.nt + hc) * p.rows_pad + row] = make_float2(m, s);
       } else if constexpr (EPI == E_STORE || EPI == E_DLOGITS) {
         float nlse = 0.f, rs = 0.f, tl = 0.f;
         int tgt = -1;
@@ -462,18 +501,21 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
           nlse = -p.lse[row] * kLog2e;
           rs = p.row_scale[row];
           tl = p.target_sum[row];
-          tgt = p.targets[row] - p.col0 - w.nt * TILE - hc * CM;
+          tgt = p.targets[row] - p.col0 - w.nt * TN - hc * CW;
         }
 #pragma unroll 1
-        for (int blk = 0; blk < 2; ++blk) {
-          if (lane == 0) bulk_wait_read<1>();  // this block's last store has left it
+        for (int blk = 0; blk < CW / 64; ++blk) {
+          // the staging blocks alternate over the warp's stores: this one's last
+          // store has left it
+          sb ^= 1;
+          if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
 #pragma unroll
           for (int h2 = 0; h2 < 2; ++h2) {
-            const int c = 64 * blk + 32 * h2;  // within this warp's 128 columns
+            const int c = 64 * blk + 32 * h2;  // within this warp's columns
             uint32_t v[32];
-            load32(hc * CM + c, v);
-            if (blk == 1 && h2 == 1) release();
+            load32(hc * CW + c, v);
+            if (blk == CW / 64 - 1 && h2 == 1) release();
             if (EPI == E_DLOGITS) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
@@ -493,7 +535,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
                   v[i] = __float_as_uint(__uint_as_float(v[i]) * scale);
               }
               if (p.residual && row < p.M) {
-                const int col = w.nt * TILE + hc * CM + c;
+                const int col = w.nt * TN + hc * CW + c;
                 const float* r = p.residual + (size_t)row * p.N + col;
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
@@ -515,25 +557,26 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
               o.y = pack2<T>(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3]));
               o.z = pack2<T>(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5]));
               o.w = pack2<T>(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7]));
-              stage16(blk, 4 * h2 + j, o);
+              stage16(sb, 4 * h2 + j, o);
             }
           }
           fence_proxy_async();
           __syncwarp();
-          const int col0 = w.nt * TILE + hc * CM + 64 * blk;
-          if (lane == 0 && row_w < (EPI == E_DLOGITS ? p.rows_pad : p.M) && col0 < p.N) {
-            tma_store_2d(&dmap0, stg + blk * STG, col0, row_w);
-            bulk_commit();
+          const int col0 = w.nt * TN + hc * CW + 64 * blk;
+          if (lane == 0) {
+            if (row_w < (EPI == E_DLOGITS ? p.rows_pad : p.M) && col0 < p.N)
+              tma_store_2d(&dmap0, stg + sb * STG, col0, row_w);
+            bulk_commit();  // a group per turn, stored or not: the wait above counts them
           }
         }
       } else {
         // E_SWIGLU: this warp's 64 gate columns and the same 64 up columns;
-        // E_SWIGLU_BWD: its 128 columns of dh, 64 at a time.
+        // E_SWIGLU_BWD: its columns of dh, 64 at a time.
         // Staging blocks: 0 = h, 1 = gate (gradient), 2 = up (gradient).
-        constexpr int BLKS = EPI == E_SWIGLU ? 1 : 2;
+        constexpr int BLKS = CW / 64;
 #pragma unroll 1
         for (int blk = 0; blk < BLKS; ++blk) {
-          const int c0 = (EPI == E_SWIGLU ? 64 * hc : CM * hc + 64 * blk);  // in the tile
+          const int c0 = CW * hc + 64 * blk;  // in the tile
           const int col0 = w.nt * NCOLS + c0;                               // of h
           if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
@@ -543,7 +586,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
             if constexpr (EPI == E_SWIGLU) {
               uint32_t vg[32], vu[32];
               load32(c0 + 32 * h2, vg);
-              load32(CM + c0 + 32 * h2, vu);
+              load32(TN / 2 + c0 + 32 * h2, vu);
               if (h2 == 1) release();
 #pragma unroll
               for (int i = 0; i < 32; i += 2) {
@@ -574,7 +617,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
               }
               uint32_t v[32];
               load32(c0 + 32 * h2, v);
-              if (blk == 1 && h2 == 1) release();
+              if (blk == BLKS - 1 && h2 == 1) release();
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const uint4 g4 = gv[i >> 2], u4 = uv[i >> 2];
@@ -638,7 +681,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
-                 "r"(512));
+                 "r"(2 * TN));
   }
 }
 
@@ -682,8 +725,9 @@ struct Operand {
   int64_t rows, k, ld;  // ld: elements between consecutive lines of memory
 };
 template <typename T, bool MN>
-inline bool operand_map(CUtensorMap* m, const Operand& o) {
-  return MN ? map_2d<T>(m, o.p, o.k, o.rows, o.ld, GK) : map_2d<T>(m, o.p, o.rows, o.k, o.ld, CM);
+inline bool operand_map(CUtensorMap* m, const Operand& o, int box_rows) {
+  return MN ? map_2d<T>(m, o.p, o.k, o.rows, o.ld, GK)
+            : map_2d<T>(m, o.p, o.rows, o.k, o.ld, box_rows);
 }
 
 // Pairs of CTAs that fit on the device at once (one CTA per SM).
@@ -719,15 +763,15 @@ inline int max_pairs(const void* kern, size_t smem) {
   return n;
 }
 
-template <typename T, bool AMN, bool BMN, int EPI>
+template <typename T, bool AMN, bool BMN, int EPI, int TN>
 cudaError_t launch_gemm_maps(const CUtensorMap& am, const CUtensorMap& bm, const CUtensorMap& d0,
                              const CUtensorMap& d1, const GemmArgs& p, cudaStream_t s) {
-  auto kern = dense_gemm_kernel<T, AMN, BMN, EPI>;
+  auto kern = dense_gemm_kernel<T, AMN, BMN, EPI, TN>;
   const void* kp = reinterpret_cast<const void*>(kern);
-  const size_t smem = sizeof(GemmSmemFor<EPI>) + 1024;
+  const size_t smem = sizeof(GemmSmemFor<EPI, TN>) + 1024;
   cudaError_t err = set_max_dynamic_smem_once(kp, (int)smem);
   if (err != cudaSuccess) return err;
-  const int64_t units = (int64_t)p.m_tiles * p.n_tiles * p.splits;
+  const int64_t units = (int64_t)p.m_tiles * p.n_tiles * std::max(p.splits, p.most_splits);
   if (units > INT32_MAX / 2) return cudaErrorInvalidValue;
   const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(max_pairs(kp, smem), units));
   cudaLaunchConfig_t cfg = {};
@@ -748,31 +792,50 @@ cudaError_t launch_gemm_maps(const CUtensorMap& am, const CUtensorMap& bm, const
 }
 
 // The GEMM on two plain operands; d0 / d1 are the epilogue's output maps.
-template <typename T, bool AMN, bool BMN, int EPI>
+template <typename T, bool AMN, bool BMN, int EPI, int TN>
 cudaError_t launch_gemm(const Operand& a, const Operand& b, const CUtensorMap& d0,
                         const CUtensorMap& d1, const GemmArgs& p, cudaStream_t s) {
   CUtensorMap am, bm;
-  if (!operand_map<T, AMN>(&am, a) || !operand_map<T, BMN>(&bm, b)) return cudaErrorInvalidValue;
-  return launch_gemm_maps<T, AMN, BMN, EPI>(am, bm, d0, d1, p, s);
+  if (!operand_map<T, AMN>(&am, a, CM) || !operand_map<T, BMN>(&bm, b, TN / 2))
+    return cudaErrorInvalidValue;
+  return launch_gemm_maps<T, AMN, BMN, EPI, TN>(am, bm, d0, d1, p, s);
 }
 
 inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// Splits of the reduction for a GEMM of `tiles` tiles and k_stages stages, at
-// most `most` (what the workspace holds).  Modelled in units of one stage's
-// MMAs (0.27 us): a pair's rounds of (stages + 6 to fill and drain), and with
-// more than one split the second kernel and the partial sums' way through L2.
-inline int pick_splits(int tiles, int k_stages, int most, bool direct_needs_finish) {
-  const int pairs = std::max(1, device_sm_count() / 2);
-  int best = 1;
+// Pairs of CTAs of the current device (two SMs each), as the plans count them.
+inline int device_pairs() { return std::max(1, device_sm_count() / 2); }
+
+// Tile width and k splits of one product.
+struct Plan {
+  int tn, splits;
+};
+// Modelled time of a product of `rows` x `cols` over `k_stages` stages, in
+// microseconds.  A stage of a 256-row tile costs its MMAs (0.27 us at 256
+// columns; at 128 the shared-memory reads of A bound it) or, where few
+// row tiles share a column tile, its operands' way from memory at this pair's
+// share of 6.4 TB/s; a unit costs about 1 us more to fill and drain.  Splits
+// cost the joining launch (3 us) and their partial sums' way through L2.
+inline Plan plan_product(int64_t rows, int64_t cols, int k_stages, int most_tiles) {
+  const int pairs = device_pairs(), mt = ceil_div(rows, TILE);
+  Plan best = {TILE, 1};
   double best_cost = 1e30;
-  for (int sp = 1; sp <= most && sp <= k_stages; ++sp) {
-    const int kps = ceil_div(k_stages, sp);
-    if (ceil_div(k_stages, kps) != sp) continue;  // an empty last split
-    const double rounds = ceil_div((int64_t)tiles * sp, pairs);
-    double cost = rounds * (kps + 6);
-    if (sp > 1 || direct_needs_finish) cost += 10.0 + 0.2 * tiles * sp / 4.0;
-    if (cost < best_cost) { best_cost = cost; best = sp; }
+  for (int tn = TILE; tn >= 128; tn /= 2) {
+    const int tiles = mt * ceil_div(cols, tn);
+    const double mma = tn == 256 ? 0.27 : 0.15;
+    const double bytes = 128.0 * (std::min<int64_t>(rows, TILE) + tn) / std::min(mt, 4);
+    const double stage = std::max(mma, bytes / (6.4e6 / pairs));
+    for (int sp = 1; sp <= 16 && sp <= k_stages; ++sp) {
+      if (sp > 1 && (tn != TILE || tiles * sp > most_tiles)) break;
+      const int kps = ceil_div(k_stages, sp);
+      if (ceil_div(k_stages, kps) != sp) continue;  // an empty last split
+      double cost = ceil_div((int64_t)tiles * sp, pairs) * (kps * stage + 1.0 + 0.004 * tn);
+      if (sp > 1) cost += 3.0 + 0.03 * tiles * sp;
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = {tn, sp};
+      }
+    }
   }
   return best;
 }
@@ -787,6 +850,9 @@ enum Finish {
 struct FinishArgs {
   const float* part;  // [split][tile][256 columns][256 rows]
   int splits, n_tiles;
+  // most_splits > 0: the splits as dense_gemm_kernel picked them for *rows
+  int most_splits, k_stages, pairs;
+  const int* rows;
   size_t split_stride;  // floats
   int M, N;             // rows and columns of out
   const float* residual;
@@ -819,8 +885,13 @@ __global__ void __launch_bounds__(256) finish_kernel(FinishArgs p) {
     const float* src = p.part + ((size_t)(cr >> 8) * p.n_tiles + nt) * (size_t)TILE_FLOATS +
                        (size_t)col * TILE + (cr & 255);
     float a[8] = {}, b[8] = {};
+    int splits = p.splits;
+    if (p.most_splits)
+      splits = even_splits((*p.rows + TILE - 1) / TILE * p.n_tiles, p.k_stages, p.most_splits,
+                           p.pairs);
     if (cr >= 0) {
-      for (int sp = 0; sp < p.splits; ++sp, src += p.split_stride) {
+#pragma unroll 4
+      for (int sp = 0; sp < splits; ++sp, src += p.split_stride) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           a[i] += src[(size_t)(warp + 8 * i) * TILE];

@@ -11,6 +11,7 @@
 // Backward: four launches, the first fusing the whole activation backward
 // (and h again, for dW_d) into the epilogue of dY Wd.
 #include "ffn_gemv.cuh"
+#include "skinny_gemm.cuh"
 
 namespace moe {
 namespace {
@@ -20,52 +21,60 @@ using namespace dense;
 // At most this many tiles of partial sums (256 KB each) in a workspace.
 constexpr int kPartTiles = 148;
 
-int splits_for(int tiles, int64_t K) {
-  return pick_splits(tiles, ceil_div(K, GK), std::max(1, kPartTiles / std::max(1, tiles)), false);
+Plan plan_of(int64_t rows, int64_t cols, int64_t K) {
+  return plan_product(rows, cols, ceil_div(K, GK), kPartTiles);
 }
-size_t part_bytes(int tiles, int64_t K) {
-  const int sp = splits_for(tiles, K);
-  return sp == 1 ? 0 : (size_t)sp * tiles * TILE_FLOATS * 4;
+size_t part_bytes(int64_t rows, int64_t cols, int64_t K) {
+  const Plan pl = plan_of(rows, cols, K);
+  return pl.splits == 1
+             ? 0
+             : (size_t)pl.splits * ceil_div(rows, TILE) * ceil_div(cols, TILE) * TILE_FLOATS * 4;
 }
 size_t align1k(size_t b) { return (b + 1023) & ~(size_t)1023; }
 
-void plan(GemmArgs& a, int m_tiles, int n_tiles, int64_t K, int splits) {
-  a.m_tiles = m_tiles;
-  a.n_tiles = n_tiles;
+void set_plan(GemmArgs& a, int64_t rows, int64_t cols, int64_t K, Plan pl) {
+  a.m_tiles = ceil_div(rows, TILE);
+  a.n_tiles = ceil_div(cols, pl.tn);
   a.k_stages = ceil_div(K, GK);
-  a.kps = ceil_div(a.k_stages, splits);
-  a.splits = ceil_div(a.k_stages, a.kps);
+  a.kps = ceil_div(a.k_stages, pl.splits);
+  a.splits = pl.splits;
 }
 
-// D [M, N] (16 bits) = A B^T (+ residual), split along k where the tiles alone
-// leave SMs idle.
+FinishArgs finish_of(const GemmArgs& p, int32_t* dev_err) {
+  FinishArgs f = {};
+  f.part = p.part;
+  f.splits = p.splits;
+  f.n_tiles = p.n_tiles;
+  f.split_stride = (size_t)p.m_tiles * p.n_tiles * TILE_FLOATS;
+  f.M = p.M;
+  f.N = p.N;
+  f.dev_err = dev_err;
+  return f;
+}
+
+// D [M, N] (16 bits) = A B^T (+ residual); narrower tiles, or splits along k,
+// where 256-column tiles alone leave SMs idle.
 template <typename T, bool AMN, bool BMN>
 cudaError_t product(const Operand& a, const Operand& b, void* d, const float* residual, float* part,
                     int32_t* dev_err, cudaStream_t s) {
-  const int mt = ceil_div(a.rows, TILE), nt = ceil_div(b.rows, TILE);
+  const Plan pl = plan_of(a.rows, b.rows, a.k);
   GemmArgs p = {};
   p.N = (int)b.rows;
   p.M = (int)a.rows;
   p.dev_err = dev_err;
-  plan(p, mt, nt, a.k, splits_for(mt * nt, a.k));
+  set_plan(p, a.rows, b.rows, a.k, pl);
   CUtensorMap dm;
   if (!map_2d<T>(&dm, d, a.rows, b.rows, b.rows, 32)) return cudaErrorInvalidValue;
-  if (p.splits == 1) {
+  if (pl.splits == 1) {
     p.residual = residual;
-    return launch_gemm<T, AMN, BMN, E_STORE>(a, b, dm, dm, p, s);
+    if (pl.tn == 128) return launch_gemm<T, AMN, BMN, E_STORE, 128>(a, b, dm, dm, p, s);
+    return launch_gemm<T, AMN, BMN, E_STORE, 256>(a, b, dm, dm, p, s);
   }
   p.part = part;
-  if (cudaError_t e = launch_gemm<T, AMN, BMN, E_PART>(a, b, dm, dm, p, s)) return e;
-  FinishArgs f = {};
-  f.part = part;
-  f.splits = p.splits;
-  f.n_tiles = nt;
-  f.split_stride = (size_t)mt * nt * TILE_FLOATS;
-  f.M = p.M;
-  f.N = p.N;
+  if (cudaError_t e = launch_gemm<T, AMN, BMN, E_PART, 256>(a, b, dm, dm, p, s)) return e;
+  FinishArgs f = finish_of(p, dev_err);
   f.residual = residual;
   f.out = d;
-  f.dev_err = dev_err;
   return launch_finish<T, F_PLAIN>(f, s);
 }
 
@@ -84,91 +93,62 @@ cudaError_t forward(const void* X, const void* W_gu, const void* W_d, int M, int
     return launch_ffn_gemv<T, 1>(X, W_gu, W_d, M, H, I, residual, Y, gu, h, dev_err, s);
   if (M <= kGemvRows)
     return launch_ffn_gemv<T, 2>(X, W_gu, W_d, M, H, I, residual, Y, gu, h, dev_err, s);
+  if (M <= kSkinnyRows) {
+    SkinnyArgs a = {};
+    a.M = M;
+    a.dev_err = dev_err;
+    a.out = h;
+    a.out1 = gu;
+    cudaError_t e = launch_skinny<T, false, S_SWIGLU>({W_gu, I, H, H}, X, H, M, a, s);
+    if (e) return e;
+    a.early = 1;
+    a.out = Y;
+    a.residual = residual;
+    return launch_skinny<T, false, S_STORE>({W_d, H, I, I}, h, I, M, a, s);
+  }
   float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + align1k((size_t)M * I * 2));
-  const int mt = ceil_div(M, TILE), nt = ceil_div(I, TILE / 2);
+  const Plan pl = plan_of(M, 2 * (int64_t)I, H);
   GemmArgs p = {};
   p.N = I;
   p.M = M;
   p.dev_err = dev_err;
   p.save = gu != nullptr;
-  plan(p, mt, nt, H, splits_for(mt * nt, H));
+  set_plan(p, M, 2 * (int64_t)I, H, pl);
+  p.n_tiles = ceil_div(I, pl.tn / 2);
   CUtensorMap am, bm, hm, gm;
-  // W_gu as [2][I][H]: box = 64 k x 128 rows of one half
+  // W_gu as [2][I][H]: box = 64 k x half a tile's rows of gate or of up
   if (!map_2d<T>(&am, X, M, H, H, CM) ||
-      !map_3d<T>(&bm, W_gu, {H, I, 2}, {H, (int64_t)I * H}, {64, CM, 1}) ||
+      !map_3d<T>(&bm, W_gu, {H, I, 2}, {H, (int64_t)I * H}, {64, pl.tn / 2, 1}) ||
       !map_2d<T>(&hm, h, M, I, I, 32))
     return cudaErrorInvalidValue;
   gm = hm;
   if (gu && !gate_up_map<T>(&gm, gu, M, I)) return cudaErrorInvalidValue;
   cudaError_t e;
-  if (p.splits == 1) {
-    e = launch_gemm_maps<T, false, false, E_SWIGLU>(am, bm, hm, gm, p, s);
-  } else {
+  if (pl.splits > 1) {
     p.part = part;
     p.gate_up = 1;
-    e = launch_gemm_maps<T, false, false, E_PART>(am, bm, hm, hm, p, s);
+    e = launch_gemm_maps<T, false, false, E_PART, 256>(am, bm, hm, hm, p, s);
     if (e) return e;
-    FinishArgs f = {};
-    f.part = part;
-    f.splits = p.splits;
-    f.n_tiles = nt;
-    f.split_stride = (size_t)mt * nt * TILE_FLOATS;
-    f.M = M;
-    f.N = I;
+    FinishArgs f = finish_of(p, dev_err);
     f.out = h;
     f.out1 = gu;
-    f.dev_err = dev_err;
     e = launch_finish<T, F_SWIGLU>(f, s);
+  } else if (pl.tn == 128) {
+    e = launch_gemm_maps<T, false, false, E_SWIGLU, 128>(am, bm, hm, gm, p, s);
+  } else {
+    e = launch_gemm_maps<T, false, false, E_SWIGLU, 256>(am, bm, hm, gm, p, s);
   }
   if (e) return e;
   return product<T, false, false>({h, M, I, I}, {W_d, H, I, I}, Y, residual, part, dev_err, s);
 }
 
+// dW_gu = dgu^T X, dW_d = dY^T h; either may be null.
 template <typename T>
-cudaError_t backward(const void* dY, const void* X, const void* gu, const void* W_gu,
-                     const void* W_d, int M, int H, int I, void* dX, void* dW_gu, void* dW_d,
-                     void* ws, int32_t* dev_err, cudaStream_t s) {
-  char* w = static_cast<char*>(ws);
-  void* h = w;
-  void* dgu = w + align1k((size_t)M * I * 2);
-  float* part = reinterpret_cast<float*>(static_cast<char*>(dgu) + align1k((size_t)M * 2 * I * 2));
-  const int mt = ceil_div(M, TILE), nt = ceil_div(I, TILE);
-  GemmArgs p = {};
-  p.N = I;
-  p.M = M;
-  p.dev_err = dev_err;
-  p.gu = gu;
-  plan(p, mt, nt, H, splits_for(mt * nt, H));
-  const Operand a = {dY, M, H, H}, b = {W_d, I, H, I};  // b: column i of W_d [H, I]
-  CUtensorMap hm, gm;
-  if (!map_2d<T>(&hm, h, M, I, I, 32) || !gate_up_map<T>(&gm, dgu, M, I))
-    return cudaErrorInvalidValue;
-  cudaError_t e;
-  if (p.splits == 1) {
-    e = launch_gemm<T, false, true, E_SWIGLU_BWD>(a, b, hm, gm, p, s);
-  } else {
-    p.part = part;
-    e = launch_gemm<T, false, true, E_PART>(a, b, hm, hm, p, s);
-    if (e) return e;
-    FinishArgs f = {};
-    f.part = part;
-    f.splits = p.splits;
-    f.n_tiles = nt;
-    f.split_stride = (size_t)mt * nt * TILE_FLOATS;
-    f.M = M;
-    f.N = I;
-    f.gu = gu;
-    f.out = h;
-    f.out1 = dgu;
-    f.dev_err = dev_err;
-    e = launch_finish<T, F_SWIGLU_BWD>(f, s);
-  }
-  if (e) return e;
+cudaError_t weight_gradients(const void* dY, const void* X, const void* h, const void* dgu, int M,
+                             int H, int I, void* dW_gu, void* dW_d, float* part, int32_t* dev_err,
+                             cudaStream_t s) {
   const int64_t I2 = 2 * (int64_t)I;
-  if (dX) {
-    e = product<T, false, true>({dgu, M, I2, I2}, {W_gu, H, I2, H}, dX, nullptr, part, dev_err, s);
-    if (e) return e;
-  }
+  cudaError_t e;
   if (dW_gu) {
     e = product<T, true, true>({dgu, I2, M, I2}, {X, H, M, H}, dW_gu, nullptr, part, dev_err, s);
     if (e) return e;
@@ -180,6 +160,66 @@ cudaError_t backward(const void* dY, const void* X, const void* gu, const void* 
   return cudaSuccess;
 }
 
+template <typename T>
+cudaError_t backward(const void* dY, const void* X, const void* gu, const void* W_gu,
+                     const void* W_d, int M, int H, int I, void* dX, void* dW_gu, void* dW_d,
+                     void* ws, int32_t* dev_err, cudaStream_t s) {
+  char* w = static_cast<char*>(ws);
+  void* h = w;
+  void* dgu = w + align1k((size_t)M * I * 2);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(dgu) + align1k((size_t)M * 2 * I * 2));
+  const int64_t I2 = 2 * (int64_t)I;
+  cudaError_t e;
+  if (M <= kSkinnyRows) {
+    SkinnyArgs a = {};
+    a.M = M;
+    a.dev_err = dev_err;
+    a.gu = gu;
+    a.out = h;
+    a.out1 = dgu;
+    e = launch_skinny<T, true, S_SWIGLU_BWD>({W_d, I, H, I}, dY, H, M, a, s);
+    if (e) return e;
+    if (dX) {
+      a.early = 1;
+      a.out = dX;
+      e = launch_skinny<T, true, S_STORE>({W_gu, H, I2, H}, dgu, I2, M, a, s);
+      if (e) return e;
+    }
+    return weight_gradients<T>(dY, X, h, dgu, M, H, I, dW_gu, dW_d, part, dev_err, s);
+  }
+  const Plan pl = plan_of(M, I, H);
+  GemmArgs p = {};
+  p.N = I;
+  p.M = M;
+  p.dev_err = dev_err;
+  p.gu = gu;
+  set_plan(p, M, I, H, pl);
+  const Operand a = {dY, M, H, H}, b = {W_d, I, H, I};  // b: column i of W_d [H, I]
+  CUtensorMap hm, gm;
+  if (!map_2d<T>(&hm, h, M, I, I, 32) || !gate_up_map<T>(&gm, dgu, M, I))
+    return cudaErrorInvalidValue;
+  if (pl.splits > 1) {
+    p.part = part;
+    e = launch_gemm<T, false, true, E_PART, 256>(a, b, hm, hm, p, s);
+    if (e) return e;
+    FinishArgs f = finish_of(p, dev_err);
+    f.gu = gu;
+    f.out = h;
+    f.out1 = dgu;
+    e = launch_finish<T, F_SWIGLU_BWD>(f, s);
+  } else if (pl.tn == 128) {
+    e = launch_gemm<T, false, true, E_SWIGLU_BWD, 128>(a, b, hm, gm, p, s);
+  } else {
+    e = launch_gemm<T, false, true, E_SWIGLU_BWD, 256>(a, b, hm, gm, p, s);
+  }
+  if (e) return e;
+  if (dX) {
+    e = product<T, false, true>({dgu, M, I2, I2}, {W_gu, H, I2, H}, dX, nullptr, part, dev_err, s);
+    if (e) return e;
+  }
+  return weight_gradients<T>(dY, X, h, dgu, M, H, I, dW_gu, dW_d, part, dev_err, s);
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -187,17 +227,14 @@ namespace moe_launch {
 using namespace moe;
 
 size_t gated_ffn_forward_workspace(int M, int H, int I) {
-  const int mt = ceil_div(M, TILE);
-  if (M <= kGemvRows) return align1k((size_t)M * I * 2);
-  return align1k((size_t)M * I * 2) + std::max(part_bytes(mt * ceil_div(I, TILE / 2), H),
-                                               part_bytes(mt * ceil_div(H, TILE), I));
+  const size_t h = align1k((size_t)M * I * 2);
+  if (M <= kSkinnyRows) return h;
+  return h + std::max(part_bytes(M, 2 * (int64_t)I, H), part_bytes(M, H, I));
 }
 size_t gated_ffn_backward_workspace(int M, int H, int I) {
-  const int mt = ceil_div(M, TILE), ht = ceil_div(H, TILE), it = ceil_div(I, TILE);
   const int64_t I2 = 2 * (int64_t)I;
-  const size_t part = std::max(std::max(part_bytes(mt * it, H), part_bytes(mt * ht, I2)),
-                               std::max(part_bytes(ceil_div(I2, TILE) * ht, M),
-                                        part_bytes(ht * it, M)));
+  const size_t part = std::max(std::max(part_bytes(M, I, H), part_bytes(M, H, I2)),
+                               std::max(part_bytes(I2, H, M), part_bytes(H, I, M)));
   return align1k((size_t)M * I * 2) + align1k((size_t)M * I * 4) + part;
 }
 

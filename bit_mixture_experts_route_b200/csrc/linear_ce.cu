@@ -18,7 +18,7 @@
 // the piece are written at once.  dl enters them as (p - [v = y]) * dloss /
 // max|dloss| (fp16: times 2^15, so that probabilities down to 2e-9 stay normal
 // numbers), and the factor comes back in fp32 at the end.
-#include "dense_gemm.cuh"
+#include "skinny_gemm.cuh"
 
 namespace moe {
 namespace {
@@ -39,7 +39,7 @@ struct Meta {
 // copies its X, target and gradient scale to its place and computes its
 // target's logit in fp32; if not, the slot writes a zero row behind the last
 // place, up to the end of that 256-row tile.  inv[t] = place or -1; row_of by
-// place; loss and lse of the other rows are 0.
+// place; loss and lse (and, where given, dX) of the other rows are 0.
 //
 // The target's logit is computed here, not taken from the tensor cores' sums:
 // those round toward zero at every step (about 2e-6 relative at 2048 terms),
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(256) ce_gather_kernel(
     int* __restrict__ inv, int* __restrict__ row_of, uint4* __restrict__ Xc,
     int* __restrict__ ctarget, float* __restrict__ ctsum, float* __restrict__ clse,
     float* __restrict__ cscale, float* __restrict__ loss, float* __restrict__ lse,
-    int32_t* dev_err) {
+    uint4* __restrict__ dX, int32_t* dev_err) {
   __shared__ int s_all[8], s_before[8];
   __shared__ float s_big[8];
   pdl_wait();
@@ -121,12 +121,17 @@ __global__ void __launch_bounds__(256) ce_gather_kernel(
       const bool keep = (kept >> j) & 1u;
       const int y = __shfl_sync(0xffffffffu, y_l, j);
       const int at = keep ? rank : all + (t - rank);
-      if (!keep && t < rows_all && lane == 0) {
-        inv[t] = -1;
-        if (loss) {
-          loss[t] = 0.0f;
-          lse[t] = 0.0f;
+      if (!keep && t < rows_all) {
+        if (lane == 0) {
+          inv[t] = -1;
+          if (loss) {
+            loss[t] = 0.0f;
+            lse[t] = 0.0f;
+          }
         }
+        if (dX)
+          for (int i = lane; i < vecs; i += 32)
+            dX[(size_t)t * vecs + i] = make_uint4(0, 0, 0, 0);
       }
       if (!keep && at >= end) continue;
       uint4* dst = Xc + (size_t)at * vecs;
@@ -204,10 +209,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ce_join_kernel(
   __syncthreads();
   if (warp == 0 && at < rows) {
     for (int w = 1; w < kJoinWarps; ++w) join(part[w][lane]);
-    const float z = m + logf(s);
+    const float ls = logf(s);
     const int t = row_of[at];
-    loss[t] = z - tsum[at];
-    lse[t] = z;
+    loss[t] = (m - tsum[at]) + ls;  // not lse - target: a confident row would lose lse's rounding
+    lse[t] = m + ls;
   }
 }
 
@@ -216,7 +221,8 @@ size_t align1k(size_t b) { return (b + 1023) & ~(size_t)1023; }
 // Layout of both workspaces.
 struct Space {
   size_t meta, inv, row_of, ctarget, clse, cscale, xc, stats, tsum, dl, part, total;
-  int rows_pad, piece, pieces, splits;
+  int rows_pad, piece, pieces, most_splits;
+  bool skinny;  // few rows, one piece: skinny_gemm.cuh
 };
 // Vocabulary columns of one piece: dl of all rows within kPieceBytes, the
 // pieces as even as whole 256-column tiles allow.
@@ -236,6 +242,7 @@ Space space_of(int T, int H, int V, bool backward) {
   w.tsum = take((size_t)w.rows_pad * 4);
   w.xc = take((size_t)w.rows_pad * H * 2);
   if (!backward) {
+    w.skinny = T <= kSkinnyRows;
     w.stats = take((size_t)2 * ceil_div(V, TILE) * w.rows_pad * sizeof(float2));
   } else {
     w.clse = take((size_t)w.rows_pad * 4);
@@ -246,10 +253,12 @@ Space space_of(int T, int H, int V, bool backward) {
     w.piece = ceil_div(ceil_div(V, w.pieces), TILE) * TILE;
     w.pieces = ceil_div(V, w.piece);
     w.dl = take((size_t)w.rows_pad * w.piece * 2);
-    const int tiles = w.rows_pad / TILE * ceil_div(H, TILE);
-    const int ks = ceil_div(std::min(V, w.piece), GK);
-    w.splits = pick_splits(tiles, ks, std::max(1, kPartTiles / tiles), true);
-    w.part = take((size_t)w.splits * tiles * TILE_FLOATS * 4);
+    w.skinny = T <= kSkinnyRows && w.pieces == 1;
+    if (!w.skinny) {
+      const int tiles = w.rows_pad / TILE * ceil_div(H, TILE);
+      w.most_splits = std::min(16, std::max(4, kPartTiles / tiles));
+      w.part = take((size_t)w.most_splits * tiles * TILE_FLOATS * 4);
+    }
   }
   w.total = at;
   return w;
@@ -258,7 +267,7 @@ Space space_of(int T, int H, int V, bool backward) {
 template <typename T>
 cudaError_t gather(const Space& w, char* ws, const void* X, const void* W, const int* targets,
                    int rows, int H, int V, int ignore_index, const float* dloss,
-                   const float* lse_in, float* loss, float* lse, int32_t* dev_err,
+                   const float* lse_in, float* loss, float* lse, void* dX, int32_t* dev_err,
                    cudaStream_t s) {
   const float unit = std::is_same<T, __half>::value ? 32768.0f : 1.0f;
   // rows per block: each block reads all targets, so more of them per block
@@ -271,7 +280,8 @@ cudaError_t gather(const Space& w, char* ws, const void* X, const void* W, const
                     reinterpret_cast<int*>(ws + w.row_of), reinterpret_cast<uint4*>(ws + w.xc),
                     reinterpret_cast<int*>(ws + w.ctarget), reinterpret_cast<float*>(ws + w.tsum),
                     reinterpret_cast<float*>(ws + w.clse),
-                    reinterpret_cast<float*>(ws + w.cscale), loss, lse, dev_err);
+                    reinterpret_cast<float*>(ws + w.cscale), loss, lse,
+                    static_cast<uint4*>(dX), dev_err);
 }
 
 template <typename T>
@@ -280,32 +290,73 @@ cudaError_t forward(const void* X, const void* W, const int* targets, int rows, 
                     cudaStream_t s) {
   const Space w = space_of(rows, H, V, false);
   cudaError_t e = gather<T>(w, ws, X, W, targets, rows, H, V, ignore_index, nullptr, nullptr,
-                            loss, lse, dev_err, s);
+                            loss, lse, nullptr, dev_err, s);
   if (e) return e;
   const Meta* meta = reinterpret_cast<const Meta*>(ws + w.meta);
-  GemmArgs p = {};
-  p.N = V;
-  p.M = rows;
-  p.m_tiles = w.rows_pad / TILE;
-  p.n_tiles = ceil_div(V, TILE);
-  p.k_stages = p.kps = ceil_div(H, GK);
-  p.splits = 1;
-  p.rows = &meta->rows;
-  p.dyn = 1;
-  p.stats = reinterpret_cast<float2*>(ws + w.stats);
-  p.target_sum = reinterpret_cast<const float*>(ws + w.tsum);
-  p.targets = reinterpret_cast<const int*>(ws + w.ctarget);
-  p.rows_pad = w.rows_pad;
-  p.dev_err = dev_err;
-  CUtensorMap am, bm;
-  if (!map_2d<T>(&am, ws + w.xc, w.rows_pad, H, H, CM) || !map_2d<T>(&bm, W, V, H, H, CM))
-    return cudaErrorInvalidValue;
-  e = launch_gemm_maps<T, false, false, E_STATS>(am, bm, am, am, p, s);
+  float2* stats = reinterpret_cast<float2*>(ws + w.stats);
+  const float* tsum = reinterpret_cast<const float*>(ws + w.tsum);
+  const int* ctarget = reinterpret_cast<const int*>(ws + w.ctarget);
+  int pieces;  // of a row's statistics
+  if (w.skinny) {
+    SkinnyArgs a = {};
+    a.M = rows;
+    a.live = &meta->rows;
+    a.early = 1;
+    a.stats = stats;
+    a.rows_pad = w.rows_pad;
+    a.target_sum = tsum;
+    a.targets = ctarget;
+    a.dev_err = dev_err;
+    pieces = ceil_div(V, CM);
+    e = launch_skinny<T, false, S_STATS>({W, V, H, H}, ws + w.xc, H, w.rows_pad, a, s);
+  } else {
+    GemmArgs p = {};
+    p.N = V;
+    p.M = rows;
+    p.m_tiles = w.rows_pad / TILE;
+    p.n_tiles = ceil_div(V, TILE);
+    p.k_stages = p.kps = ceil_div(H, GK);
+    p.splits = 1;
+    p.rows = &meta->rows;
+    p.dyn = 1;
+    p.stats = stats;
+    p.target_sum = tsum;
+    p.targets = ctarget;
+    p.rows_pad = w.rows_pad;
+    p.dev_err = dev_err;
+    pieces = 2 * p.n_tiles;
+    CUtensorMap am, bm;
+    if (!map_2d<T>(&am, ws + w.xc, w.rows_pad, H, H, CM) || !map_2d<T>(&bm, W, V, H, H, CM))
+      return cudaErrorInvalidValue;
+    e = launch_gemm_maps<T, false, false, E_STATS, 256>(am, bm, am, am, p, s);
+  }
   if (e) return e;
   return launch_pdl(ce_join_kernel, dim3(w.rows_pad / 32), dim3(32 * kJoinWarps), 0, s,
-                    static_cast<const float2*>(p.stats), 2 * p.n_tiles, w.rows_pad,
-                    p.target_sum, meta,
+                    static_cast<const float2*>(stats), pieces, w.rows_pad, tsum, meta,
                     reinterpret_cast<const int*>(ws + w.row_of), loss, lse);
+}
+
+// Rows [v0, v0 + vn) of dW = dl^T X, from the first `reach` rows of dl.
+template <typename T>
+cudaError_t head_gradient(const Space& w, char* ws, int v0, int vn, int reach, int H, void* dW,
+                          int32_t* dev_err, cudaStream_t s) {
+  const Meta* meta = reinterpret_cast<const Meta*>(ws + w.meta);
+  GemmArgs q = {};
+  q.N = H;
+  q.M = vn;
+  q.m_tiles = ceil_div(vn, TILE);
+  q.n_tiles = ceil_div(H, TILE);
+  q.k_stages = q.kps = ceil_div(reach, GK);
+  q.splits = 1;
+  q.rows = &meta->rows;
+  q.dyn = 2;
+  q.scale = &meta->out_scale;
+  q.dev_err = dev_err;
+  CUtensorMap om;
+  if (!map_2d<T>(&om, static_cast<char*>(dW) + (size_t)v0 * H * 2, vn, H, H, 32))
+    return cudaErrorInvalidValue;
+  return launch_gemm<T, true, true, E_STORE, 256>({ws + w.dl, vn, reach, w.piece},
+                                                  {ws + w.xc, H, w.rows_pad, H}, om, om, q, s);
 }
 
 template <typename T>
@@ -314,13 +365,37 @@ cudaError_t backward(const float* dloss, const void* X, const void* W, const int
                      void* dW, char* ws, int32_t* dev_err, cudaStream_t s) {
   const Space w = space_of(rows, H, V, true);
   cudaError_t e = gather<T>(w, ws, X, W, targets, rows, H, V, ignore_index, dloss, lse, nullptr,
-                            nullptr, dev_err, s);
+                            nullptr, w.skinny ? dX : nullptr, dev_err, s);
   if (e) return e;
   const Meta* meta = reinterpret_cast<const Meta*>(ws + w.meta);
+  if (w.skinny) {
+    SkinnyArgs a = {};
+    a.M = rows;
+    a.live = &meta->rows;
+    a.early = 1;
+    a.dev_err = dev_err;
+    a.out = ws + w.dl;
+    a.ld = w.piece;
+    a.targets = reinterpret_cast<const int*>(ws + w.ctarget);
+    a.lse = reinterpret_cast<const float*>(ws + w.clse);
+    a.row_scale = reinterpret_cast<const float*>(ws + w.cscale);
+    a.target_sum = reinterpret_cast<const float*>(ws + w.tsum);
+    e = launch_skinny<T, false, S_DLOGITS>({W, V, H, H}, ws + w.xc, H, w.rows_pad, a, s);
+    if (e) return e;
+    if (dX) {
+      a.out = dX;
+      a.scale = &meta->out_scale;
+      a.row_of = reinterpret_cast<const int*>(ws + w.row_of);
+      e = launch_skinny<T, true, S_STORE>({W, H, V, H}, ws + w.dl, w.piece, w.rows_pad, a, s);
+      if (e) return e;
+    }
+    // dl has the rows that the product's tokens fill; behind them nothing is read
+    return dW ? head_gradient<T>(w, ws, 0, V, (rows + 31) / 32 * 32, H, dW, dev_err, s)
+              : cudaSuccess;
+  }
   const int mt = w.rows_pad / TILE, ht = ceil_div(H, TILE);
   char* dl = ws + w.dl;
   float* part = reinterpret_cast<float*>(ws + w.part);
-  int splits = 0;
   for (int i = 0; i < w.pieces; ++i) {
     const int v0 = i * w.piece, vn = std::min(w.piece, V - v0);
     const char* Wi = static_cast<const char*>(W) + (size_t)v0 * H * 2;
@@ -342,7 +417,7 @@ cudaError_t backward(const float* dloss, const void* X, const void* W, const int
     p.dev_err = dev_err;
     CUtensorMap lm;
     if (!map_2d<T>(&lm, dl, w.rows_pad, vn, w.piece, 32)) return cudaErrorInvalidValue;
-    e = launch_gemm<T, false, false, E_DLOGITS>({ws + w.xc, w.rows_pad, H, H}, {Wi, vn, H, H}, lm,
+    e = launch_gemm<T, false, false, E_DLOGITS, 256>({ws + w.xc, w.rows_pad, H, H}, {Wi, vn, H, H}, lm,
                                                 lm, p, s);
     if (e) return e;
     if (dX) {
@@ -351,45 +426,33 @@ cudaError_t backward(const float* dloss, const void* X, const void* W, const int
       q.M = rows;
       q.m_tiles = mt;
       q.n_tiles = ht;
-      // every piece adds to the same splits' sums: a shorter last piece is cut
-      // anew, and a split left without stages adds zeros
-      q.k_stages = ceil_div(vn, GK);
-      if (i == 0) splits = ceil_div(q.k_stages, ceil_div(q.k_stages, w.splits));
-      q.kps = ceil_div(q.k_stages, splits);
-      q.splits = splits;
+      // every piece adds to the same splits' sums, so all run as many stages:
+      // a shorter last piece reads zeros behind its end
+      q.k_stages = w.piece / GK;
+      q.splits = 1;
+      q.most_splits = w.most_splits;
+      q.pairs = device_pairs();
       q.rows = &meta->rows;
       q.dyn = 1;
       q.part = part;
       q.accumulate = i > 0;
       q.dev_err = dev_err;
-      e = launch_gemm<T, false, true, E_PART>({dl, w.rows_pad, vn, w.piece}, {Wi, H, vn, H}, lm,
+      e = launch_gemm<T, false, true, E_PART, 256>({dl, w.rows_pad, vn, w.piece}, {Wi, H, vn, H}, lm,
                                               lm, q, s);
       if (e) return e;
     }
     if (dW) {
-      GemmArgs q = {};
-      q.N = H;
-      q.M = vn;
-      q.m_tiles = ceil_div(vn, TILE);
-      q.n_tiles = ht;
-      q.k_stages = q.kps = w.rows_pad / GK;
-      q.splits = 1;
-      q.rows = &meta->rows;
-      q.dyn = 2;
-      q.scale = &meta->out_scale;
-      q.dev_err = dev_err;
-      CUtensorMap om;
-      if (!map_2d<T>(&om, static_cast<char*>(dW) + (size_t)v0 * H * 2, vn, H, H, 32))
-        return cudaErrorInvalidValue;
-      e = launch_gemm<T, true, true, E_STORE>({dl, vn, w.rows_pad, w.piece},
-                                              {ws + w.xc, H, w.rows_pad, H}, om, om, q, s);
+      e = head_gradient<T>(w, ws, v0, vn, w.rows_pad, H, dW, dev_err, s);
       if (e) return e;
     }
   }
   if (!dX) return cudaSuccess;
   FinishArgs f = {};
   f.part = part;
-  f.splits = splits;
+  f.most_splits = w.most_splits;
+  f.k_stages = w.piece / GK;
+  f.pairs = device_pairs();
+  f.rows = &meta->rows;
   f.n_tiles = ht;
   f.split_stride = (size_t)mt * ht * TILE_FLOATS;
   f.M = rows;

@@ -1,0 +1,490 @@
+// Products of a weight matrix with few tokens (17 to 128), on the tensor cores:
+//   D[t, n] = sum_k X[t, k] W[n, k],  W either way round,
+// the form that the feed-forward block and the vocabulary cross entropy take
+// for a decode batch.  Such a product is bound by reading W once, so the roles
+// of the operands are swapped against dense_gemm.cuh: 128 rows of W are the
+// MMA's M, the tokens its N (32 to 128 columns), and a stage is 16 KB of W with
+// 4 to 16 KB of tokens, where a 256-row tile of mostly absent tokens would
+// fill as much shared memory with zeros as with weights.
+//
+// Work split.  A tile of W is 128 rows.  Where the tiles alone leave SMs idle,
+// a cluster of 2, 4 or 8 CTAs shares one tile along k; each CTA leaves its fp32
+// sums in its shared memory and joins its share of the tokens from all CTAs of
+// the cluster through distributed shared memory, in rank order, so the result
+// does not depend on timing and nothing goes through global memory or a second
+// launch.  Persistent: a cluster walks tiles, and the tensor memory holds two
+// accumulators, so that loads and MMAs of the next tile run under the join.
+//
+// Warp roles (384 threads): warp 0 loads (TMA), warp 1 issues the MMAs and owns
+// the tensor memory, warps 4-11 move sums to shared memory (two per TMEM lane
+// quarter) and join.  Kernels that follow another of the same call (early) load
+// the first weights before they wait for it: nothing in the call writes W.
+// Every wait is bounded as in dense_gemm.cuh.
+#pragma once
+
+#include "dense_gemm.cuh"
+
+namespace moe {
+namespace dense {
+
+constexpr int kSkinnyRows = 128;  // tokens at most
+constexpr int kSkinnyStages = 10; // at most
+
+enum SkinnyEpilogue {
+  S_STORE,       // out[row_of[t] or t] = 16-bit (sum * *scale + residual)
+  S_SWIGLU,      // tile = 64 gate rows, 64 up rows: out = h, out1 = gate | up (if given)
+  S_SWIGLU_BWD,  // sums are dh: out = h, out1 = dgate | dup, from gu
+  S_STATS,       // per token and tile: maximum and sum of exponentials
+  S_DLOGITS,     // out = (exp(sum - lse) - [column is the target]) * row scale
+};
+
+struct SkinnyArgs {
+  int n;         // tokens, rounded up to 32
+  int M;         // tokens
+  const int* live;  // device: tokens that count (<= M), or null: M
+  int rows;      // columns of the result (S_SWIGLU: of h)
+  int tiles, k_stages, stages, early;
+  const float* residual;
+  const float* scale;
+  const int* row_of;
+  const void* gu;
+  void* out;
+  void* out1;
+  int ld;        // S_DLOGITS: elements per row of out
+  float2* stats; // [tile][rows_pad]
+  int rows_pad;
+  const float* target_sum;
+  const int* targets;
+  const float* lse;
+  const float* row_scale;
+  int32_t* dev_err;
+};
+
+struct SkinnyBars {
+  uint64_t full[kSkinnyStages], empty[kSkinnyStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t ready, taken;  // the sums of all CTAs stand / have been read by all
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+__host__ __device__ constexpr int skinny_stage(int n) { return CM * GK * 2 + n * GK * 2; }
+__host__ __device__ constexpr int skinny_sums(int n) { return n * CM * 4; }
+constexpr int kSkinnySmem = 227 * 1024;
+inline int skinny_stages(int n) {
+  const int room = kSkinnySmem - 1024 - (int)sizeof(SkinnyBars) - skinny_sums(n);
+  return std::min(kSkinnyStages, room / skinny_stage(n));
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void mma_ss_one(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ float4 lds_cluster4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+template <typename T, bool AMN, int EPI>
+__global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
+    const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+    const __grid_constant__ SkinnyArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const int NS = p.stages, STAGE = skinny_stage(p.n), N = p.n;
+  float* sums = reinterpret_cast<float*>(ring + NS * STAGE);  // [token][128 rows of W]
+  SkinnyBars& sm = *reinterpret_cast<SkinnyBars*>(ring + NS * STAGE + skinny_sums(N));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank(), cs = (int)cluster_size();
+  const uint32_t tmem_cols = N <= 16 ? 32u : N <= 32 ? 64u : N <= 64 ? 128u : 256u;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&sm.acc_full[a], 1);
+      mbar_init(&sm.acc_empty[a], EPI_NW);
+    }
+    mbar_init(&sm.ready, EPI_NW * cs);
+    mbar_init(&sm.taken, EPI_NW * cs);
+    mbar_init(&sm.drain, 1);
+    sm.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&sm.tmem_base)),
+                 "r"(tmem_cols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = sm.tmem_base;
+
+  // this CTA's stages of every tile, and the tiles of its cluster
+  const int k0 = (int)((int64_t)p.k_stages * rank / cs);
+  const int k1 = (int)((int64_t)p.k_stages * (rank + 1) / cs);
+  const int t0 = blockIdx.x / cs, tstep = gridDim.x / cs;
+
+  if (warp == 0) {
+    // ---------------- TMA producer
+    if (lane == 0) {
+      auto load_w = [&](int s, int tile, int k) {
+        uint8_t* a = ring + s * STAGE;
+        mbar_arrive_expect_tx(&sm.full[s], (uint32_t)STAGE);
+        if (EPI == S_SWIGLU) {  // 64 gate rows, 64 up rows
+          tma_load_3d(a, &wmap, &sm.full[s], k * GK, tile * 64, 0);
+          tma_load_3d(a + OPERAND / 2, &wmap, &sm.full[s], k * GK, tile * 64, 1);
+        } else if (AMN) {
+          tma_load_2d(a, &wmap, &sm.full[s], tile * CM, k * GK);
+          tma_load_2d(a + OPERAND / 2, &wmap, &sm.full[s], tile * CM + 64, k * GK);
+        } else {
+          tma_load_2d(a, &wmap, &sm.full[s], k * GK, tile * CM);
+        }
+      };
+      auto load_x = [&](int s, int k) {
+        tma_load_2d(ring + s * STAGE + OPERAND, &xmap, &sm.full[s], k * GK, 0);
+      };
+      // the first tile's first stages: their slots are free from the start
+      const int early = p.early && t0 < p.tiles ? min(NS, k1 - k0) : 0;
+      for (int i = 0; i < early; ++i) load_w(i, t0, k0 + i);
+      pdl_wait();
+      pdl_trigger();
+      const bool some = p.live == nullptr || *p.live > 0;
+      int s = 0, issued = 0;
+      uint32_t ph = 0;
+      for (int i = 0; i < early; ++i) {
+        load_x(i, k0 + i);
+        ++issued;
+        if (++s == NS) { s = 0; ph ^= 1; }
+      }
+      bool ok = true;
+      for (int tile = t0; tile < p.tiles && some && ok; tile += tstep) {
+        for (int k = k0 + (tile == t0 ? early : 0); k < k1; ++k) {
+          if (!(ok = mbar_wait(&sm.empty[s], ph ^ 1, sm, p.dev_err))) break;
+          load_w(s, tile, k);
+          load_x(s, k);
+          ++issued;
+          if (++s == NS) { s = 0; ph ^= 1; }
+        }
+      }
+      // every copy that was requested has landed before the CTA may leave
+      for (int i = 0; i < min(issued, NS); ++i) {
+        if (--s < 0) { s = NS - 1; ph ^= 1; }
+        for (uint32_t n = 0; n < kWaitLimit && !mbar_try_wait_suspend(&sm.full[s], ph); ++n) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer
+    if (lane == 0) {
+      pdl_wait();
+      const bool some = p.live == nullptr || *p.live > 0;
+      const uint32_t f = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+      const uint32_t idesc = (1u << 4) | (f << 7) | (f << 10) | ((AMN ? 1u : 0u) << 15) |
+                             ((uint32_t)(N >> 3) << 17) | ((uint32_t)(CM >> 4) << 24);
+      const uint64_t ad0 = operand_desc<AMN>(smem_u32(ring));
+      const uint64_t bd0 = operand_desc<false>(smem_u32(ring) + OPERAND);
+      int s = 0, lt = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int tile = t0; tile < p.tiles && some && ok; tile += tstep, ++lt) {
+        const int acc = lt & 1;
+        if (!(ok = mbar_poll(&sm.acc_empty[acc], ((lt >> 1) & 1) ^ 1, sm, p.dev_err))) break;
+        tc_fence_after();
+        const uint32_t dcol = tmem_base + acc * N;
+        for (int k = k0; k < k1; ++k) {
+          if (!(ok = mbar_poll(&sm.full[s], ph, sm, p.dev_err))) break;
+          tc_fence_after();
+          const uint64_t ad = ad0 + (uint64_t)((s * STAGE) >> 4);
+          const uint64_t bd = bd0 + (uint64_t)((s * STAGE) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < GK / 16; ++kk)
+            mma_ss_one(dcol, ad + kk * kstep_units<AMN>(), bd + kk * kstep_units<false>(), idesc,
+                       (k != k0 || kk != 0) ? 1u : 0u);
+          mma_commit(&sm.empty[s]);
+          if (++s == NS) { s = 0; ph ^= 1; }
+        }
+        if (ok) mma_commit(&sm.acc_full[acc]);
+      }
+      // every MMA issued here is done with the shared memory before the CTA leaves
+      mma_commit(&sm.drain);
+      for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait_suspend(&sm.drain, 0); ++i) {
+      }
+    }
+  } else if (warp >= EPI_W0) {
+    // ---------------- sums to shared memory, join, epilogue
+    pdl_wait();
+    const int tokens = p.live ? min(*p.live, p.M) : p.M;
+    // S_DLOGITS also writes the rows behind the last token, as zeros: dW's reduction reads them
+    const int joined = EPI == S_DLOGITS ? N : tokens;
+    const int ew = warp - EPI_W0, q = warp & 3, hc = ew >> 2;
+    const uint32_t lane_addr = (uint32_t)(32 * q) << 16;
+    const float scale = (EPI == S_STORE && p.scale) ? *p.scale : 1.0f;
+    bool ovf = false;
+    int lt = 0;
+    uint32_t bases[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) bases[r] = cluster_addr(sums, r < cs ? r : rank);
+    for (int tile = t0; tile < p.tiles && tokens > 0; tile += tstep, ++lt) {
+      const int acc = lt & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.acc_full[acc], (lt >> 1) & 1, sm, p.dev_err)))
+        break;
+      tc_fence_after();
+      // all CTAs have read the tile before
+      if (!__all_sync(0xffffffffu, mbar_wait<true>(&sm.taken, (lt & 1) ^ 1, sm, p.dev_err))) break;
+      for (int c = hc; c < N / 32; c += 2) {
+        uint32_t v[32];
+        tmem_ld32(tmem_base + lane_addr + acc * N + 32 * c, v);
+        float* d = sums + (size_t)(32 * c) * CM + 32 * q + lane;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) d[i * CM] = __uint_as_float(v[i]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.acc_empty[acc]);
+      if (lane < cs) {
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        mbar_arrive_remote(cluster_addr(&sm.ready, lane));
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait<true>(&sm.ready, lt & 1, sm, p.dev_err))) break;
+
+      // tokens rank + cs * (ew + 8 i) of this tile
+      auto sum4 = [&](int t, int row) {  // 4 rows from `row` on
+        const uint32_t at = (uint32_t)(t * CM + row) * 4u;
+        float4 a = lds_cluster4(bases[0] + at);
+#pragma unroll
+        for (int r = 1; r < 8; ++r)
+          if (r < cs) {
+            const float4 b = lds_cluster4(bases[r] + at);
+            a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+          }
+        return a;
+      };
+#pragma unroll 2
+      for (int t = rank + cs * ew; t < joined; t += cs * EPI_NW) {
+        if constexpr (EPI == S_SWIGLU) {
+          // lanes 0-15 hold gate columns 4 lane .., lanes 16-31 the same up columns
+          const float4 v = sum4(t, 4 * lane);
+          const int col = tile * 64 + 4 * (lane & 15);
+          const float vs[4] = {v.x, v.y, v.z, v.w};
+          float o[4], h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = __shfl_down_sync(0xffffffffu, vs[e], 16);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = __fdividef(vs[e], 1.0f + __expf(-vs[e])) * o[e];
+          if (col < p.rows) {  // a multiple of 8
+            if (lane < 16) {
+              ovf |= overflows_out<T>(h[0]) | overflows_out<T>(h[1]) | overflows_out<T>(h[2]) |
+                     overflows_out<T>(h[3]);
+              *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (size_t)t * p.rows + col) =
+                  make_uint2(pack2<T>(h[0], h[1]), pack2<T>(h[2], h[3]));
+            }
+            if (p.out1) {
+              ovf |= overflows_out<T>(vs[0]) | overflows_out<T>(vs[1]) |
+                     overflows_out<T>(vs[2]) | overflows_out<T>(vs[3]);
+              *reinterpret_cast<uint2*>(static_cast<T*>(p.out1) + (size_t)t * 2 * p.rows +
+                                        (lane < 16 ? 0 : p.rows) + col) =
+                  make_uint2(pack2<T>(vs[0], vs[1]), pack2<T>(vs[2], vs[3]));
+            }
+          }
+        } else {
+          const int col = tile * CM + 4 * lane;
+          const float4 v4 = sum4(t, 4 * lane);
+          float v[4] = {v4.x, v4.y, v4.z, v4.w};
+          if constexpr (EPI == S_STORE) {
+            if (col < p.rows) {
+              const size_t at = (size_t)(p.row_of ? p.row_of[t] : t) * p.rows + col;
+              if (p.scale) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] *= scale;
+              }
+              if (p.residual) {
+                const float4 r = *reinterpret_cast<const float4*>(p.residual + at);
+                v[0] += r.x; v[1] += r.y; v[2] += r.z; v[3] += r.w;
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) ovf |= overflows_out<T>(v[e]);
+              *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at) =
+                  make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
+            }
+          } else if constexpr (EPI == S_SWIGLU_BWD) {
+            if (col < p.rows) {
+              const size_t at = (size_t)t * p.rows + col, at2 = (size_t)t * 2 * p.rows + col;
+              const T* gu = static_cast<const T*>(p.gu) + at2;
+              const uint2 gw = *reinterpret_cast<const uint2*>(gu);
+              const uint2 uw = *reinterpret_cast<const uint2*>(gu + p.rows);
+              const float2 ga = unpack2<T>(gw.x), gb = unpack2<T>(gw.y);
+              const float2 ua = unpack2<T>(uw.x), ub = unpack2<T>(uw.y);
+              const float g[4] = {ga.x, ga.y, gb.x, gb.y}, uu[4] = {ua.x, ua.y, ub.x, ub.y};
+              float h[4], dg[4], du[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float s = __fdividef(1.0f, 1.0f + __expf(-g[e])), sg = g[e] * s;
+                h[e] = sg * uu[e];
+                du[e] = v[e] * sg;
+                dg[e] = v[e] * uu[e] * (s + sg * (1.0f - s));
+                ovf |= overflows_out<T>(du[e]) | overflows_out<T>(dg[e]) | overflows_out<T>(h[e]);
+              }
+              T* d = static_cast<T*>(p.out1) + at2;
+              *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at) =
+                  make_uint2(pack2<T>(h[0], h[1]), pack2<T>(h[2], h[3]));
+              *reinterpret_cast<uint2*>(d) =
+                  make_uint2(pack2<T>(dg[0], dg[1]), pack2<T>(dg[2], dg[3]));
+              *reinterpret_cast<uint2*>(d + p.rows) =
+                  make_uint2(pack2<T>(du[0], du[1]), pack2<T>(du[2], du[3]));
+            }
+          } else if constexpr (EPI == S_STATS) {
+            const int tgt = p.targets[t] - col;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (tgt == e) v[e] = p.target_sum[t];
+              if (col + e >= p.rows) v[e] = -INFINITY;
+            }
+            const float m = warp_max(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
+            const float s = warp_sum((exp2_approx((v[0] - m) * kLog2e) +
+                                      exp2_approx((v[1] - m) * kLog2e)) +
+                                     (exp2_approx((v[2] - m) * kLog2e) +
+                                      exp2_approx((v[3] - m) * kLog2e)));
+            if (lane == 0) p.stats[(size_t)tile * p.rows_pad + t] = make_float2(m, s);
+          } else {  // S_DLOGITS
+            const float nlse = -p.lse[t] * kLog2e, rs = p.row_scale[t];
+            const int tgt = p.targets[t] - col;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float x = exp2_approx(fmaf(v[e], kLog2e, nlse));
+              if (tgt == e) x = exp2_approx(fmaf(p.target_sum[t], kLog2e, nlse)) - 1.0f;
+              v[e] = x * rs;
+            }
+            // rows of out are p.ld >= 128 tiles long: the last tile's end is theirs too
+            *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (size_t)t * p.ld + col) =
+                make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
+          }
+        }
+      }
+      __syncwarp();
+      if (lane < cs) {
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        mbar_arrive_remote(cluster_addr(&sm.taken, lane));
+      }
+    }
+    __syncwarp();
+    if (__any_sync(0xffffffffu, ovf) && lane == 0) set_dev_err(p.dev_err, MOE_DEVERR_RANGE);
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // nobody leaves while a peer may read its sums or arrive on its barriers
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"(tmem_cols));
+  }
+}
+
+// Clusters of c CTAs that fit on the device at once.
+inline int max_clusters(const void* kern, int c) {
+  static std::mutex mu;
+  static std::unordered_map<uint64_t, int> cache;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  const uint64_t key = (reinterpret_cast<uint64_t>(kern) << 10) ^ (uint64_t)(dev << 4) ^ (uint64_t)c;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    const auto it = cache.find(key);
+    if (it != cache.end()) return it->second;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(c * std::max(1, device_sm_count() / c));
+  cfg.blockDim = dim3(GEMM_THREADS);
+  cfg.dynamicSmemBytes = kSkinnySmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = c;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    n = std::max(1, device_sm_count() / c);
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  cache[key] = n;
+  return n;
+}
+
+// W: rows x k (S_SWIGLU: [2][rows][k]); X [M, k] with ldx elements per row.
+template <typename T, bool AMN, int EPI>
+cudaError_t launch_skinny(const Operand& w, const void* X, int64_t ldx, int x_rows, SkinnyArgs p,
+                          cudaStream_t s) {
+  auto kern = skinny_gemm_kernel<T, AMN, EPI>;
+  const void* kp = reinterpret_cast<const void*>(kern);
+  if (cudaError_t e = set_max_dynamic_smem_once(kp, kSkinnySmem)) return e;
+  p.n = (p.M + 31) / 32 * 32;
+  p.stages = skinny_stages(p.n);
+  p.rows = (int)w.rows;
+  p.tiles = ceil_div(w.rows, EPI == S_SWIGLU ? 64 : CM);
+  p.k_stages = ceil_div(w.k, GK);
+  CUtensorMap wm, xm;
+  const bool mapped =
+      EPI == S_SWIGLU
+          ? map_3d<T>(&wm, w.p, {w.k, w.rows, 2}, {w.ld, w.rows * w.ld}, {GK, 64, 1})
+          : operand_map<T, AMN>(&wm, w, CM);
+  if (!mapped || !map_2d<T>(&xm, X, x_rows, w.k, ldx, p.n)) return cudaErrorInvalidValue;
+  int best = 1;
+  double best_cost = 1e30;
+  for (int c = 1; c <= 8 && c <= p.k_stages; c *= 2) {
+    if (EPI == S_STATS && c > 1) break;
+    const int fit = max_clusters(kp, c);
+    // rounds of the busiest cluster, each its stages and about `fixed` more
+    const double cost = (double)ceil_div(p.tiles, fit) * ((double)ceil_div(p.k_stages, c) + 5.0);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = c;
+    }
+  }
+#ifdef SKINNY_C
+  best = SKINNY_C;
+#endif
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(best * std::min(p.tiles, max_clusters(kp, best)));
+  cfg.blockDim = dim3(GEMM_THREADS);
+  cfg.dynamicSmemBytes = kSkinnySmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = best;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, wm, xm, p);
+}
+
+}  // namespace dense
+}  // namespace moe
