@@ -542,26 +542,35 @@ def layer_forward(X, logits, k, renormalize, packed_gu, absmax_gu, packed_d, abs
 _HALF = (torch.bfloat16, torch.float16)
 
 
-class _on:
-    """``with _on(device)``: the device of the tensors is current."""
+# The cheap ways to the current device and stream, where this torch has them: a
+# small call's time is mostly its host side.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-    def __init__(self, device):
-        self.guard = None
-        if device.type == "cuda" and device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
+
+class _Here:
+    """``with _on(device)`` where the device is the current one already."""
 
     def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
+        return self
 
     def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        return False
+
+
+_HERE_ALREADY = _Here()
+
+
+def _on(device):
+    """``with _on(device)``: the device of the tensors is current."""
+    if device.index is None or device.index == _current_device():
+        return _HERE_ALREADY
+    return torch.cuda.device(device)
 
 
 def _matrix(t, shape, name, dtype, device):
     """``t`` is a contiguous tensor of exactly this shape, type and device."""
-    if t is None or (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype
+    if t is None or (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype
                      and t.shape == shape and t.device == device and t.is_contiguous()):
         return
     _need(t, dtype, name)
@@ -573,12 +582,14 @@ def _matrix(t, shape, name, dtype, device):
 
 def _raw_stream(device):
     """The address of ``device``'s current stream; the cheap way where there is one."""
-    if device.type == "cuda" and _current_raw_stream is not None:
+    if device.index is not None and _current_raw_stream is not None:
         return _current_raw_stream(device.index)
     return _stream(device)
 
 
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+def _at(t):
+    """A tensor's address, None for none."""
+    return None if t is None else t.data_ptr()
 
 
 def _dev_word(dev_err, device):
@@ -598,7 +609,7 @@ def _size(fn, *args):
 
 def _space(workspace, nbytes, device):
     if workspace is None:
-        return torch.empty((max(nbytes, 256),), dtype=torch.uint8, device=device)
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
     _room(workspace, nbytes, "workspace", (torch.uint8,))
     if workspace.device != device:
         raise MoEError(f"workspace is on {workspace.device}, the call's tensors are on {device}")
@@ -636,19 +647,22 @@ def gated_ffn_forward(X, W_gu, W_d, residual=None, save_gu=False, workspace=None
     pre-activations ``[T, 2I]`` that the backward call reads."""
     T, H, I = _ffn_shapes(X, W_gu, W_d)
     dev = X.device
-    _matrix(residual, (T, H), "residual", torch.float32, dev)
-    _matrix(out, (T, H), "out", X.dtype, dev)
-    _matrix(gu, (T, 2 * I), "gu", X.dtype, dev)
+    if residual is not None:
+        _matrix(residual, (T, H), "residual", torch.float32, dev)
+    if out is not None:
+        _matrix(out, (T, H), "out", X.dtype, dev)
+    if gu is not None:
+        _matrix(gu, (T, 2 * I), "gu", X.dtype, dev)
     _dev_word(dev_err, dev)
     with _on(dev):
         ws = _space(workspace, gated_ffn_forward_workspace_size(T, H, I), dev)
         if out is None:
-            out = torch.empty((T, H), dtype=X.dtype, device=dev)
+            out = torch.empty_like(X)
         if gu is None and save_gu:
-            gu = torch.empty((T, 2 * I), dtype=X.dtype, device=dev)
+            gu = X.new_empty((T, 2 * I))
         _check(load().moe_gated_ffn_forward(
-            _ptr(X), DT[X.dtype], _ptr(W_gu), _ptr(W_d), T, H, I, _ptr(residual), _ptr(out),
-            _ptr(gu), _ptr(ws), ws.numel(), _ptr(dev_err), _raw_stream(dev)), "moe_gated_ffn_forward")
+            _at(X), DT[X.dtype], _at(W_gu), _at(W_d), T, H, I, _at(residual), _at(out),
+            _at(gu), _at(ws), ws.numel(), _at(dev_err), _raw_stream(dev)), "moe_gated_ffn_forward")
     return out if gu is None else (out, gu)
 
 
@@ -670,8 +684,8 @@ def gated_ffn_backward(dY, X, gu, W_gu, W_d, need_dx=True, need_dw=True, workspa
         dW_gu = torch.empty_like(W_gu) if need_dw else None
         dW_d = torch.empty_like(W_d) if need_dw else None
         _check(load().moe_gated_ffn_backward(
-            _ptr(dY), DT[X.dtype], _ptr(X), _ptr(gu), _ptr(W_gu), _ptr(W_d), T, H, I, _ptr(dX),
-            _ptr(dW_gu), _ptr(dW_d), _ptr(ws), ws.numel(), _ptr(dev_err), _raw_stream(dev)),
+            _at(dY), DT[X.dtype], _at(X), _at(gu), _at(W_gu), _at(W_d), T, H, I, _at(dX),
+            _at(dW_gu), _at(dW_d), _at(ws), ws.numel(), _at(dev_err), _raw_stream(dev)),
             "moe_gated_ffn_backward")
     return dX, dW_gu, dW_d
 
@@ -707,11 +721,11 @@ def linear_ce_forward(X, W, targets, ignore_index=-100, workspace=None, dev_err=
     _dev_word(dev_err, dev)
     with _on(dev):
         ws = _space(workspace, linear_ce_forward_workspace_size(T, H, V), dev)
-        loss = torch.empty((T,), dtype=torch.float32, device=dev)
-        lse = torch.empty((T,), dtype=torch.float32, device=dev)
+        loss = torch.empty(T, dtype=torch.float32, device=dev)
+        lse = torch.empty_like(loss)
         _check(load().moe_linear_ce_forward(
-            _ptr(X), DT[X.dtype], _ptr(W), _ptr(targets), T, H, V, ignore_index, _ptr(loss),
-            _ptr(lse), _ptr(ws), ws.numel(), _ptr(dev_err), _raw_stream(dev)),
+            _at(X), DT[X.dtype], _at(W), _at(targets), T, H, V, ignore_index, _at(loss),
+            _at(lse), _at(ws), ws.numel(), _at(dev_err), _raw_stream(dev)),
             "moe_linear_ce_forward")
     return loss, lse
 
@@ -733,8 +747,8 @@ def linear_ce_backward(dloss, X, W, targets, lse, ignore_index=-100, need_dx=Tru
         dX = torch.empty_like(X) if need_dx else None
         dW = torch.empty_like(W) if need_dw else None
         _check(load().moe_linear_ce_backward(
-            _ptr(dloss), _ptr(X), DT[X.dtype], _ptr(W), _ptr(targets), _ptr(lse), T, H, V,
-            ignore_index, _ptr(dX), _ptr(dW), _ptr(ws), ws.numel(), _ptr(dev_err), _raw_stream(dev)),
+            _at(dloss), _at(X), DT[X.dtype], _at(W), _at(targets), _at(lse), T, H, V,
+            ignore_index, _at(dX), _at(dW), _at(ws), ws.numel(), _at(dev_err), _raw_stream(dev)),
             "moe_linear_ce_backward")
     return dX, dW
 
@@ -788,8 +802,8 @@ def grad_norm_clip(grads, max_norm, norm=None, workspace=None, dev_err=None):
     with _on(dev):
         ws = _space(workspace, grads.nbytes, dev)
         if norm is None:
-            norm = torch.empty((1,), dtype=torch.float32, device=dev)
+            norm = torch.empty(1, dtype=torch.float32, device=dev)
         _check(load().moe_grad_norm_clip(
-            grads._in, grads._numel, grads._dt, grads.n, max_norm, grads._out, _ptr(norm),
-            _ptr(ws), ws.numel(), _ptr(dev_err), _raw_stream(dev)), "moe_grad_norm_clip")
+            grads._in, grads._numel, grads._dt, grads.n, max_norm, grads._out, _at(norm),
+            _at(ws), ws.numel(), _at(dev_err), _raw_stream(dev)), "moe_grad_norm_clip")
     return norm

@@ -61,10 +61,14 @@ constexpr bool is_swiglu(int epi) { return epi == E_SWIGLU || epi == E_SWIGLU_BW
 constexpr int halves_of(int epi, int tn) {
   return epi == E_SWIGLU ? tn / 128 : 2;
 }
-constexpr int stg_of(int epi) {  // staging blocks per epilogue warp
-  return is_swiglu(epi) ? 3 : (epi == E_PART || epi == E_STATS) ? 0 : 2;
+// Bytes of staging per epilogue warp: one block of 64 columns that the warp's
+// stores take in turn (E_SWIGLU_BWD: three of 32 columns).  More would cost an
+// operand stage, and the loads' way from L2 needs them more: at 4096 x 2048 x
+// 8192, 4 stages kept the tensor cores 71 % busy, 5 stages 87 %.
+constexpr int stg_of(int epi) {
+  return epi == E_SWIGLU_BWD ? 3 * STG / 2 : (epi == E_PART || epi == E_STATS) ? 0 : STG;
 }
-constexpr int stg_bytes(int epi, int tn) { return 4 * halves_of(epi, tn) * stg_of(epi) * STG; }
+constexpr int stg_bytes(int epi, int tn) { return 4 * halves_of(epi, tn) * stg_of(epi); }
 // As many stages as the shared memory holds beside the staging blocks.
 constexpr int kSmemBudget = 227 * 1024 - 1024 - 512;
 constexpr int stages_of(int epi, int tn) {
@@ -90,6 +94,7 @@ struct GemmArgs {
   int M;
   const void* gu;        // E_SWIGLU_BWD: [M, 2N] gate | up
   int save;              // E_SWIGLU: write D1
+  int early;             // B is an input of the whole call: load its first stages at once
   int gate_up;           // E_PART: B and the columns as in E_SWIGLU
   float2* stats;         // E_STATS: [2 n_tiles][rows_pad]
   const float* target_sum;  // E_STATS, E_DLOGITS: the target column's sum of each row
@@ -104,7 +109,7 @@ struct GemmArgs {
 template <int NS, int SB, int NW, int NSTG>
 struct __align__(8) GemmSmem {
   uint8_t ab[NS][SB];  // 1024-aligned
-  uint8_t stg[NW][NSTG > 0 ? NSTG : 1][NSTG > 0 ? STG : 16];
+  uint8_t stg[NW][NSTG > 0 ? NSTG : 16];
   uint64_t full[NS], empty[NS];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
@@ -148,6 +153,15 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
+// 1 / (1 + exp(-x)) by the fast exponential and reciprocal, relative error about
+// 1e-6, far below a 16-bit rounding.  The ftz forms spend nothing on subnormal
+// arguments; where exp(-x) leaves fp32's range the result is 0.
+__device__ __forceinline__ float sigmoid_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp2_approx(-kLog2e * x)));
+  return r;
+}
+
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map,
                                                  uint32_t cluster_bar, int x, int y, int z) {
   asm volatile(
@@ -171,15 +185,18 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
       "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 __device__ __forceinline__ void bulk_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 template <int N>
 __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void bulk_wait_all() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // Shared-memory descriptor of an operand tile.  K-major: 128 rows of 128
@@ -272,6 +289,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
   const bool leader = rank == 0;
 
   if (threadIdx.x == 0) {
+    prefetch_map(&amap);
+    prefetch_map(&bmap);
     for (int s = 0; s < NS; ++s) {
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], 1);
@@ -295,6 +314,33 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = sm.tmem_base;
+  const int u0 = blockIdx.x >> 1, ustep = gridDim.x >> 1;
+  constexpr int NCOLS = EPI == E_SWIGLU ? TN / 2 : TN;  // columns of one tile
+  const bool gate_up = EPI == E_SWIGLU || (EPI == E_PART && p.gate_up);
+  auto load_b = [&](int s, const Unit& w, int k) {
+    uint8_t* b = sm.ab[s] + OPERAND;
+    const uint32_t bar = cluster_addr(&sm.full[s], 0);
+    const int brow = gate_up ? w.nt * BROWS : w.nt * TN + rank * BROWS;
+    if (gate_up) {  // gate rows in the leader, up rows in its peer
+      tma_load_3d_pair(b, &bmap, bar, k * GK, brow, rank);
+    } else if (BMN) {
+      tma_load_2d_pair(b, &bmap, bar, brow, k * GK);
+      if (BROWS > 64) tma_load_2d_pair(b + OPERAND / 2, &bmap, bar, brow + 64, k * GK);
+    } else {
+      tma_load_2d_pair(b, &bmap, bar, k * GK, brow);
+    }
+  };
+  // the first unit's first stages: their slots are free from the start, and
+  // what the kernel before writes is not B (the host sets early without dyn)
+  int early = 0;
+  if (p.early && warp == 0 && lane == 0 && u0 < p.m_tiles * p.n_tiles * p.splits) {
+    const Unit w = unit_of(u0, p.m_tiles, p.n_tiles, p.k_stages, p.kps);
+    early = min(NS, w.k1 - w.k0);
+    for (int i = 0; i < early; ++i) {
+      if (leader) mbar_arrive_expect_tx(&sm.full[i], 2 * STAGE);
+      load_b(i, w, w.k0 + i);
+    }
+  }
   pdl_wait();
   pdl_trigger();
 
@@ -307,14 +353,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
       kps = max(1, (k_stages + p.splits - 1) / p.splits);
     }
   }
-  const int u0 = blockIdx.x >> 1, ustep = gridDim.x >> 1;
   if (EPI == E_PART && p.most_splits) {
     splits = even_splits(m_tiles * p.n_tiles, k_stages, p.most_splits, p.pairs);
     kps = (k_stages + splits - 1) / splits;
   }
   const int units = m_tiles * p.n_tiles * splits;
-  constexpr int NCOLS = EPI == E_SWIGLU ? TN / 2 : TN;  // columns of one tile
-  const bool gate_up = EPI == E_SWIGLU || (EPI == E_PART && p.gate_up);
 
   if (warp == 0) {
     // ---------------- TMA producer
@@ -325,27 +368,23 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
       for (int u = u0; u < units && ok; u += ustep) {
         const Unit w = unit_of(u, m_tiles, p.n_tiles, k_stages, kps);
         const int arow = w.mt * TILE + rank * CM;
-        const int brow = gate_up ? w.nt * BROWS : w.nt * TN + rank * BROWS;
         for (int k = w.k0; k < w.k1; ++k) {
-          if (!(ok = mbar_wait<true>(&sm.empty[s], ph ^ 1, sm, p.dev_err))) break;
-          if (leader) mbar_arrive_expect_tx(&sm.full[s], 2 * STAGE);
+          const bool has_b = early > 0;  // B is on its way already
+          if (has_b) {
+            --early;
+          } else {
+            if (!(ok = mbar_wait<true>(&sm.empty[s], ph ^ 1, sm, p.dev_err))) break;
+            if (leader) mbar_arrive_expect_tx(&sm.full[s], 2 * STAGE);
+          }
           const uint32_t bar = cluster_addr(&sm.full[s], 0);
           uint8_t* a = sm.ab[s];
-          uint8_t* b = a + OPERAND;
           if (AMN) {
             tma_load_2d_pair(a, &amap, bar, arow, k * GK);
             tma_load_2d_pair(a + OPERAND / 2, &amap, bar, arow + 64, k * GK);
           } else {
             tma_load_2d_pair(a, &amap, bar, k * GK, arow);
           }
-          if (gate_up) {  // gate rows in the leader, up rows in its peer
-            tma_load_3d_pair(b, &bmap, bar, k * GK, brow, rank);
-          } else if (BMN) {
-            tma_load_2d_pair(b, &bmap, bar, brow, k * GK);
-            if (BROWS > 64) tma_load_2d_pair(b + OPERAND / 2, &bmap, bar, brow + 64, k * GK);
-          } else {
-            tma_load_2d_pair(b, &bmap, bar, k * GK, brow);
-          }
+          if (!has_b) load_b(s, w, k);
           ++issued;
           if (++s == NS) { s = 0; ph ^= 1; }
         }
@@ -399,20 +438,55 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
     constexpr int CW = NCOLS / HALVES;
     const int ew = warp - EPI_W0, q = warp & 3, hc = ew >> 2;
     const uint32_t lane_addr = (uint32_t)(32 * q) << 16;
-    uint8_t* stg = sm.stg[ew][0];
-    int lt = 0, sb = 0;
+    uint8_t* stg = sm.stg[ew];
+    int lt = 0;
     bool ovf = false;
     const float scale = (EPI == E_STORE && p.scale) ? *p.scale : 1.0f;
-    // 16 bytes (8 columns) of this lane's row into chunk c of a staging block
-    auto stage16 = [&](int blk, int c, uint4 v) {
-      *reinterpret_cast<uint4*>(stg + blk * STG + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
+    // 16 bytes (8 columns) of this lane's row into chunk c of the staging block
+    auto stage16 = [&](int c, uint4 v) {
+      *reinterpret_cast<uint4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
     };
+    auto stage32 = [&](int c, const uint32_t (&v)[32]) {  // 32 columns from chunk c on
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint4 o;
+        o.x = pack2<T>(__uint_as_float(v[8 * j]), __uint_as_float(v[8 * j + 1]));
+        o.y = pack2<T>(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3]));
+        o.z = pack2<T>(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5]));
+        o.w = pack2<T>(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7]));
+        stage16(c + j, o);
+      }
+    };
+    // the warp's last store has left the staging block
+    auto stage_free = [&]() {
+      if (lane == 0) bulk_wait_read<0>();
+      __syncwarp();
+    };
+    // E_SWIGLU_BWD: gate and up of the warp's 32 rows x 32 columns, four lanes
+    // a row (a lane per row would touch four times the lines per load): 16 bytes
+    // of rows lane / 4 + 8 i
+    uint4 gu_next[2][4];
+    auto load_gu = [&](int row0, int col) {
+      const int r0 = row0 + (lane >> 2), c = col + 8 * (lane & 3);
+      const T* gp = reinterpret_cast<const T*>(p.gu) + (size_t)r0 * (2 * (size_t)p.N) + c;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool in = r0 + 8 * i < p.M && c < p.N;  // N is a multiple of 8
+        const uint4* g = reinterpret_cast<const uint4*>(gp + (size_t)(16 * i) * p.N);
+        const uint4* u = reinterpret_cast<const uint4*>(gp + (size_t)(16 * i + 1) * p.N);
+        gu_next[0][i] = in ? ldg_stream_u4(g) : make_uint4(0, 0, 0, 0);
+        gu_next[1][i] = in ? ldg_stream_u4(u) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    // chunk c (16 bytes) of row r in a 64-byte-swizzled block
+    auto at64 = [](int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); };
     for (int u = u0; u < units; u += ustep, ++lt) {
       const Unit w = unit_of(u, m_tiles, p.n_tiles, k_stages, kps);
       const int acc = lt & 1;
       const int row = w.mt * TILE + rank * CM + 32 * q + lane;  // this lane's row of D
       const int row_w = row - lane;                             // the warp's first
       const bool none = w.k0 >= w.k1;  // nothing to sum: the tensor memory holds old values
+      if constexpr (EPI == E_SWIGLU_BWD) load_gu(row_w, w.nt * TN + hc * CW);  // under the MMAs
       if (!__all_sync(0xffffffffu,
                       mbar_wait<true>(&sm.acc_full[acc], (lt >> 1) & 1, sm, p.dev_err)))
         break;
@@ -505,11 +579,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
         }
 #pragma unroll 1
         for (int blk = 0; blk < CW / 64; ++blk) {
-          // the staging blocks alternate over the warp's stores: this one's last
-          // store has left it
-          sb ^= 1;
-          if (lane == 0) bulk_wait_read<1>();
-          __syncwarp();
+          stage_free();
 #pragma unroll
           for (int h2 = 0; h2 < 2; ++h2) {
             const int c = 64 * blk + 32 * h2;  // within this warp's columns
@@ -550,125 +620,127 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
 #pragma unroll
               for (int i = 0; i < 32; ++i) ovf |= overflows_out<T>(__uint_as_float(v[i]));
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint4 o;
-              o.x = pack2<T>(__uint_as_float(v[8 * j]), __uint_as_float(v[8 * j + 1]));
-              o.y = pack2<T>(__uint_as_float(v[8 * j + 2]), __uint_as_float(v[8 * j + 3]));
-              o.z = pack2<T>(__uint_as_float(v[8 * j + 4]), __uint_as_float(v[8 * j + 5]));
-              o.w = pack2<T>(__uint_as_float(v[8 * j + 6]), __uint_as_float(v[8 * j + 7]));
-              stage16(sb, 4 * h2 + j, o);
-            }
+            stage32(4 * h2, v);
           }
           fence_proxy_async();
           __syncwarp();
           const int col0 = w.nt * TN + hc * CW + 64 * blk;
-          if (lane == 0) {
-            if (row_w < (EPI == E_DLOGITS ? p.rows_pad : p.M) && col0 < p.N)
-              tma_store_2d(&dmap0, stg + sb * STG, col0, row_w);
-            bulk_commit();  // a group per turn, stored or not: the wait above counts them
+          if (lane == 0 && row_w < (EPI == E_DLOGITS ? p.rows_pad : p.M) && col0 < p.N) {
+            tma_store_2d(&dmap0, stg, col0, row_w);
+            bulk_commit();
+          }
+        }
+      } else if constexpr (EPI == E_SWIGLU) {
+        // this warp's 64 gate columns and the same 64 up columns: h, then, from
+        // the tensor memory again, gate and up
+        const int c0 = CW * hc, col0 = w.nt * NCOLS + c0;
+        stage_free();
+#pragma unroll
+        for (int h2 = 0; h2 < 2; ++h2) {
+          uint32_t vg[32], vu[32];
+          load32(c0 + 32 * h2, vg);
+          load32(TN / 2 + c0 + 32 * h2, vu);
+          if (h2 == 1 && !p.save) release();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float g = __uint_as_float(vg[i]), u = __uint_as_float(vu[i]);
+            const float h = g * sigmoid_fast(g) * u;
+            ovf |= overflows_out<T>(h);
+            vg[i] = __float_as_uint(h);
+          }
+          stage32(4 * h2, vg);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        const bool in = row_w < p.M && col0 < p.N;
+        if (lane == 0 && in) {
+          tma_store_2d(&dmap0, stg, col0, row_w);
+          bulk_commit();
+        }
+        if (p.save) {
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) {
+            stage_free();
+#pragma unroll
+            for (int h2 = 0; h2 < 2; ++h2) {
+              uint32_t v[32];
+              load32(part * (TN / 2) + c0 + 32 * h2, v);
+              if (part == 1 && h2 == 1) release();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) ovf |= overflows_out<T>(__uint_as_float(v[i]));
+              stage32(4 * h2, v);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0 && in) {
+              tma_store_3d(&dmap1, stg, col0, part, row_w);
+              bulk_commit();
+            }
           }
         }
       } else {
-        // E_SWIGLU: this warp's 64 gate columns and the same 64 up columns;
-        // E_SWIGLU_BWD: its columns of dh, 64 at a time.
-        // Staging blocks: 0 = h, 1 = gate (gradient), 2 = up (gradient).
-        constexpr int BLKS = CW / 64;
+        // E_SWIGLU_BWD: columns of dh, 32 at a time; the next 32 columns of gu
+        // are on their way meanwhile.  Staging: h, gate, up, each 32 rows of 64
+        // bytes (64-byte swizzle); the gradients take gate's and up's places
 #pragma unroll 1
-        for (int blk = 0; blk < BLKS; ++blk) {
-          const int c0 = CW * hc + 64 * blk;  // in the tile
-          const int col0 = w.nt * NCOLS + c0;                               // of h
-          if (lane == 0) bulk_wait_read<0>();
+        for (int c = 0; c < CW; c += 32) {
+          const int col0 = w.nt * TN + hc * CW + c;
+          stage_free();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = at64((lane >> 2) + 8 * i, lane & 3);
+            *reinterpret_cast<uint4*>(stg + STG / 2 + at) = gu_next[0][i];
+            *reinterpret_cast<uint4*>(stg + STG + at) = gu_next[1][i];
+          }
+          if (c + 32 < CW) load_gu(row_w, col0 + 32);
           __syncwarp();
+          uint32_t v[32];
+          load32(hc * CW + c, v);
+          if (c + 32 == CW) release();
 #pragma unroll
-          for (int h2 = 0; h2 < 2; ++h2) {
-            uint32_t ho[16], go[16], uo[16];
-            if constexpr (EPI == E_SWIGLU) {
-              uint32_t vg[32], vu[32];
-              load32(c0 + 32 * h2, vg);
-              load32(TN / 2 + c0 + 32 * h2, vu);
-              if (h2 == 1) release();
+          for (int j = 0; j < 4; ++j) {
+            uint8_t* d = stg + at64(lane, j);
+            const uint4 gv = *reinterpret_cast<const uint4*>(d + STG / 2);
+            const uint4 uv = *reinterpret_cast<const uint4*>(d + STG);
+            const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w};
+            const uint32_t uw[4] = {uv.x, uv.y, uv.z, uv.w};
+            uint32_t ho[4], go[4], uo[4];
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float g0 = __uint_as_float(vg[i]), g1 = __uint_as_float(vg[i + 1]);
-                const float u0_ = __uint_as_float(vu[i]), u1 = __uint_as_float(vu[i + 1]);
-                // silu by the fast exponential and division: relative error
-                // about 1e-6, far below the 16-bit rounding of h
-                const float h0 = __fdividef(g0, 1.0f + __expf(-g0)) * u0_;
-                const float h1 = __fdividef(g1, 1.0f + __expf(-g1)) * u1;
-                ovf |= overflows_out<T>(h0) | overflows_out<T>(h1);
-                ho[i >> 1] = pack2<T>(h0, h1);
-                go[i >> 1] = pack2<T>(g0, g1);
-                uo[i >> 1] = pack2<T>(u0_, u1);
-                if (p.save)
-                  ovf |= overflows_out<T>(g0) | overflows_out<T>(g1) | overflows_out<T>(u0_) |
-                         overflows_out<T>(u1);
+            for (int i = 0; i < 4; ++i) {
+              const float2 g2 = unpack2<T>(gw[i]), u2 = unpack2<T>(uw[i]);
+              float hh[2], dg[2], du[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float g = e ? g2.y : g2.x, uu = e ? u2.y : u2.x;
+                const float dh = __uint_as_float(v[8 * j + 2 * i + e]);
+                const float sg = sigmoid_fast(g);
+                const float si = g * sg;  // silu(g)
+                hh[e] = si * uu;
+                du[e] = dh * si;
+                dg[e] = dh * uu * (sg + si * (1.0f - sg));
+                ovf |= overflows_out<T>(du[e]) | overflows_out<T>(dg[e]) | overflows_out<T>(hh[e]);
               }
-            } else {
-              const int col = col0 + 32 * h2;
-              const T* gp = reinterpret_cast<const T*>(p.gu) + (size_t)row * (2 * (size_t)p.N) + col;
-              uint4 gv[4], uv[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const bool in = row < p.M && col + 8 * j < p.N;  // N is a multiple of 8
-                gv[j] = in ? *reinterpret_cast<const uint4*>(gp + 8 * j) : make_uint4(0, 0, 0, 0);
-                uv[j] = in ? *reinterpret_cast<const uint4*>(gp + p.N + 8 * j)
-                           : make_uint4(0, 0, 0, 0);
-              }
-              uint32_t v[32];
-              load32(c0 + 32 * h2, v);
-              if (blk == BLKS - 1 && h2 == 1) release();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const uint4 g4 = gv[i >> 2], u4 = uv[i >> 2];
-                const uint32_t gw = (i & 3) == 0 ? g4.x : (i & 3) == 1 ? g4.y : (i & 3) == 2 ? g4.z
-                                                                                             : g4.w;
-                const uint32_t uw = (i & 3) == 0 ? u4.x : (i & 3) == 1 ? u4.y : (i & 3) == 2 ? u4.z
-                                                                                             : u4.w;
-                const float2 g = unpack2<T>(gw), uu = unpack2<T>(uw);
-                float dg[2], du[2], hh[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const float gg = e ? g.y : g.x, ue = e ? uu.y : uu.x;
-                  const float dh = __uint_as_float(v[2 * i + e]);
-                  const float s = __fdividef(1.0f, 1.0f + __expf(-gg));
-                  const float sg = gg * s;  // silu(g)
-                  hh[e] = sg * ue;
-                  du[e] = dh * sg;
-                  dg[e] = dh * ue * (s + sg * (1.0f - s));
-                  ovf |= overflows_out<T>(du[e]) | overflows_out<T>(dg[e]) |
-                         overflows_out<T>(hh[e]);
-                }
-                ho[i] = pack2<T>(hh[0], hh[1]);
-                go[i] = pack2<T>(dg[0], dg[1]);
-                uo[i] = pack2<T>(du[0], du[1]);
-              }
+              ho[i] = pack2<T>(hh[0], hh[1]);
+              go[i] = pack2<T>(dg[0], dg[1]);
+              uo[i] = pack2<T>(du[0], du[1]);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              stage16(0, 4 * h2 + j, make_uint4(ho[4 * j], ho[4 * j + 1], ho[4 * j + 2], ho[4 * j + 3]));
-              if (EPI == E_SWIGLU_BWD || p.save) {
-                stage16(1, 4 * h2 + j,
-                        make_uint4(go[4 * j], go[4 * j + 1], go[4 * j + 2], go[4 * j + 3]));
-                stage16(2, 4 * h2 + j,
-                        make_uint4(uo[4 * j], uo[4 * j + 1], uo[4 * j + 2], uo[4 * j + 3]));
-              }
-            }
+            *reinterpret_cast<uint4*>(d) = make_uint4(ho[0], ho[1], ho[2], ho[3]);
+            *reinterpret_cast<uint4*>(d + STG / 2) = make_uint4(go[0], go[1], go[2], go[3]);
+            *reinterpret_cast<uint4*>(d + STG) = make_uint4(uo[0], uo[1], uo[2], uo[3]);
           }
           fence_proxy_async();
           __syncwarp();
           if (lane == 0 && row_w < p.M && col0 < p.N) {
             tma_store_2d(&dmap0, stg, col0, row_w);
-            if (EPI == E_SWIGLU_BWD || p.save) {
-              tma_store_3d(&dmap1, stg + STG, col0, 0, row_w);
-              tma_store_3d(&dmap1, stg + 2 * STG, col0, 1, row_w);
-            }
+            tma_store_3d(&dmap1, stg + STG / 2, col0, 0, row_w);
+            tma_store_3d(&dmap1, stg + STG, col0, 1, row_w);
             bulk_commit();
           }
         }
       }
     }
-    if (stg_of(EPI) > 0 && lane == 0) bulk_wait_all();
+    // the stores have read the shared memory; the kernel's end waits for their writes
+    if (stg_of(EPI) > 0 && lane == 0) bulk_wait_read<0>();
     __syncwarp();
     // the loop exits are warp-uniform, so every lane takes part
     if (__any_sync(0xffffffffu, ovf) && lane == 0) set_dev_err(p.dev_err, MOE_DEVERR_RANGE);
@@ -688,19 +760,19 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
 // ---------------------------------------------------------------- host side
 
 // Tensor map of a row-major 16-bit matrix [rows, cols] with `ld` elements per
-// row; box of 64 columns x box_rows, 128-byte swizzle.
+// row; box of 64 columns x box_rows, 128-byte swizzle (or 32 and 64 bytes).
 template <typename T>
 inline bool map_2d(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld,
-                   int box_rows) {
+                   int box_rows, int box_cols = 64) {
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, es[2] = {1, 1};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, es[2] = {1, 1};
   return encode_tiled_cached(
              m,
              std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
              2, const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 template <typename T>
@@ -715,7 +787,7 @@ inline bool map_3d(CUtensorMap* m, const void* p, const int64_t (&d)[3], const i
              std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
              3, const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             b[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -942,7 +1014,7 @@ __global__ void __launch_bounds__(256) finish_kernel(FinishArgs p) {
   } else if (FIN == F_SWIGLU) {
     float h[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = __fdividef(v[e], 1.0f + __expf(-v[e])) * w[e];
+    for (int e = 0; e < 8; ++e) h[e] = v[e] * sigmoid_fast(v[e]) * w[e];
     put(p.out, at, h);
     if (p.out1) {
       put(p.out1, at2, v);
@@ -954,7 +1026,7 @@ __global__ void __launch_bounds__(256) finish_kernel(FinishArgs p) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float g = to_f32<T>(gu[at2 + e]), u = to_f32<T>(gu[at2 + p.N + e]);
-      const float s = __fdividef(1.0f, 1.0f + __expf(-g)), sg = g * s;
+      const float s = sigmoid_fast(g), sg = g * s;
       h[e] = sg * u;
       du[e] = v[e] * sg;
       dg[e] = v[e] * u * (s + sg * (1.0f - s));

@@ -53,14 +53,16 @@ FinishArgs finish_of(const GemmArgs& p, int32_t* dev_err) {
 }
 
 // D [M, N] (16 bits) = A B^T (+ residual); narrower tiles, or splits along k,
-// where 256-column tiles alone leave SMs idle.
+// where 256-column tiles alone leave SMs idle.  early: nothing in the call
+// writes b.
 template <typename T, bool AMN, bool BMN>
 cudaError_t product(const Operand& a, const Operand& b, void* d, const float* residual, float* part,
-                    int32_t* dev_err, cudaStream_t s) {
+                    bool early, int32_t* dev_err, cudaStream_t s) {
   const Plan pl = plan_of(a.rows, b.rows, a.k);
   GemmArgs p = {};
   p.N = (int)b.rows;
   p.M = (int)a.rows;
+  p.early = early;
   p.dev_err = dev_err;
   set_plan(p, a.rows, b.rows, a.k, pl);
   CUtensorMap dm;
@@ -78,10 +80,10 @@ cudaError_t product(const Operand& a, const Operand& b, void* d, const float* re
   return launch_finish<T, F_PLAIN>(f, s);
 }
 
-// Map of [T][2][I] (gate | up rows), boxes of 64 columns x 1 x 32 rows.
+// Map of [T][2][I] (gate | up rows), boxes of `cols` columns x 1 x 32 rows.
 template <typename T>
-bool gate_up_map(CUtensorMap* m, const void* p, int64_t rows, int64_t I) {
-  return map_3d<T>(m, p, {I, 2, rows}, {I, 2 * I}, {64, 1, 32});
+bool gate_up_map(CUtensorMap* m, const void* p, int64_t rows, int64_t I, int cols) {
+  return map_3d<T>(m, p, {I, 2, rows}, {I, 2 * I}, {cols, 1, 32});
 }
 
 template <typename T>
@@ -122,7 +124,7 @@ cudaError_t forward(const void* X, const void* W_gu, const void* W_d, int M, int
       !map_2d<T>(&hm, h, M, I, I, 32))
     return cudaErrorInvalidValue;
   gm = hm;
-  if (gu && !gate_up_map<T>(&gm, gu, M, I)) return cudaErrorInvalidValue;
+  if (gu && !gate_up_map<T>(&gm, gu, M, I, 64)) return cudaErrorInvalidValue;
   cudaError_t e;
   if (pl.splits > 1) {
     p.part = part;
@@ -139,7 +141,7 @@ cudaError_t forward(const void* X, const void* W_gu, const void* W_d, int M, int
     e = launch_gemm_maps<T, false, false, E_SWIGLU, 256>(am, bm, hm, gm, p, s);
   }
   if (e) return e;
-  return product<T, false, false>({h, M, I, I}, {W_d, H, I, I}, Y, residual, part, dev_err, s);
+  return product<T, false, false>({h, M, I, I}, {W_d, H, I, I}, Y, residual, part, true, dev_err, s);
 }
 
 // dW_gu = dgu^T X, dW_d = dY^T h; either may be null.
@@ -150,11 +152,13 @@ cudaError_t weight_gradients(const void* dY, const void* X, const void* h, const
   const int64_t I2 = 2 * (int64_t)I;
   cudaError_t e;
   if (dW_gu) {
-    e = product<T, true, true>({dgu, I2, M, I2}, {X, H, M, H}, dW_gu, nullptr, part, dev_err, s);
+    e = product<T, true, true>({dgu, I2, M, I2}, {X, H, M, H}, dW_gu, nullptr, part, true,
+                               dev_err, s);
     if (e) return e;
   }
   if (dW_d) {
-    e = product<T, true, true>({dY, H, M, H}, {h, I, M, I}, dW_d, nullptr, part, dev_err, s);
+    e = product<T, true, true>({dY, H, M, H}, {h, I, M, I}, dW_d, nullptr, part, false,
+                               dev_err, s);
     if (e) return e;
   }
   return cudaSuccess;
@@ -196,7 +200,7 @@ cudaError_t backward(const void* dY, const void* X, const void* gu, const void* 
   set_plan(p, M, I, H, pl);
   const Operand a = {dY, M, H, H}, b = {W_d, I, H, I};  // b: column i of W_d [H, I]
   CUtensorMap hm, gm;
-  if (!map_2d<T>(&hm, h, M, I, I, 32) || !gate_up_map<T>(&gm, dgu, M, I))
+  if (!map_2d<T>(&hm, h, M, I, I, 32, 32) || !gate_up_map<T>(&gm, dgu, M, I, 32))
     return cudaErrorInvalidValue;
   if (pl.splits > 1) {
     p.part = part;
@@ -214,7 +218,8 @@ cudaError_t backward(const void* dY, const void* X, const void* gu, const void* 
   }
   if (e) return e;
   if (dX) {
-    e = product<T, false, true>({dgu, M, I2, I2}, {W_gu, H, I2, H}, dX, nullptr, part, dev_err, s);
+    e = product<T, false, true>({dgu, M, I2, I2}, {W_gu, H, I2, H}, dX, nullptr, part, true,
+                                dev_err, s);
     if (e) return e;
   }
   return weight_gradients<T>(dY, X, h, dgu, M, H, I, dW_gu, dW_d, part, dev_err, s);

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps) ffn_gemv_kernel(
     }
     if (UP) {
       const int j = blockIdx.x * 8 + row;
-      const float h = __fdividef(v0, 1.0f + __expf(-v0)) * v1;
+      const float h = v0 * sigmoid_fast(v0) * v1;
       ovf |= overflows_out<T>(h);
       out[(size_t)tok * rows + j] = from_f32<T>(h);
       if (gu) {

@@ -115,6 +115,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
   const uint32_t tmem_cols = N <= 16 ? 32u : N <= 32 ? 64u : N <= 64 ? 128u : 256u;
 
   if (threadIdx.x == 0) {
+    prefetch_map(&wmap);
+    prefetch_map(&xmap);
     for (int s = 0; s < NS; ++s) {
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], 1);
@@ -248,6 +250,20 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
     for (int r = 0; r < 8; ++r) bases[r] = cluster_addr(sums, r < cs ? r : rank);
     for (int tile = t0; tile < p.tiles && tokens > 0; tile += tstep, ++lt) {
       const int acc = lt & 1;
+      if constexpr (EPI == S_STORE || EPI == S_SWIGLU_BWD) {
+        // what the join will read, on its way to L2 under the MMAs
+        const int col = tile * CM + 4 * lane;
+        if (col < p.rows && (EPI == S_SWIGLU_BWD || p.residual))
+          for (int t = rank + cs * ew; t < tokens; t += cs * EPI_NW) {
+            if (EPI == S_STORE) {
+              prefetch_l2(p.residual + (size_t)t * p.rows + col);
+            } else {
+              const T* gu = static_cast<const T*>(p.gu) + (size_t)t * 2 * p.rows + col;
+              prefetch_l2(gu);
+              prefetch_l2(gu + p.rows);
+            }
+          }
+      }
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.acc_full[acc], (lt >> 1) & 1, sm, p.dev_err)))
         break;
       tc_fence_after();
@@ -263,8 +279,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.acc_empty[acc]);
-      if (lane < cs) {
-        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+      if (cs == 1) {
+        if (lane == 0) mbar_arrive(&sm.ready);
+      } else if (lane < cs) {
         mbar_arrive_remote(cluster_addr(&sm.ready, lane));
       }
       if (!__all_sync(0xffffffffu, mbar_wait<true>(&sm.ready, lt & 1, sm, p.dev_err))) break;
@@ -281,7 +298,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
           }
         return a;
       };
-#pragma unroll 2
+#pragma unroll 4
       for (int t = rank + cs * ew; t < joined; t += cs * EPI_NW) {
         if constexpr (EPI == S_SWIGLU) {
           // lanes 0-15 hold gate columns 4 lane .., lanes 16-31 the same up columns
@@ -292,7 +309,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[e] = __shfl_down_sync(0xffffffffu, vs[e], 16);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = __fdividef(vs[e], 1.0f + __expf(-vs[e])) * o[e];
+          for (int e = 0; e < 4; ++e) h[e] = vs[e] * sigmoid_fast(vs[e]) * o[e];
           if (col < p.rows) {  // a multiple of 8
             if (lane < 16) {
               ovf |= overflows_out<T>(h[0]) | overflows_out<T>(h[1]) | overflows_out<T>(h[2]) |
@@ -340,7 +357,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
               float h[4], dg[4], du[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float s = __fdividef(1.0f, 1.0f + __expf(-g[e])), sg = g[e] * s;
+                const float s = sigmoid_fast(g[e]), sg = g[e] * s;
                 h[e] = sg * uu[e];
                 du[e] = v[e] * sg;
                 dg[e] = v[e] * uu[e] * (s + sg * (1.0f - s));
@@ -382,9 +399,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
           }
         }
       }
+      if (tile + tstep >= p.tiles) break;  // nobody waits for the last tile's
       __syncwarp();
-      if (lane < cs) {
-        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+      if (cs == 1) {
+        if (lane == 0) mbar_arrive(&sm.taken);
+      } else if (lane < cs) {
         mbar_arrive_remote(cluster_addr(&sm.taken, lane));
       }
     }
