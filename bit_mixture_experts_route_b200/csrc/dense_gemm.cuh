@@ -81,8 +81,7 @@ struct GemmArgs {
   int m_tiles, n_tiles;  // tiles of 256 rows; of 256 columns (E_SWIGLU: 128)
   int k_stages;          // ceil(K / 64)
   int splits, kps;       // k splits and stages per split
-  int most_splits;       // > 0: the kernel picks the splits itself, at most so many, for
-  int pairs;             // so many pairs (E_PART)
+  const int* splits_of;  // E_PART: device word with the splits (at most `splits`), or null
   // *rows (device) replaces the row count (dyn = 1) or the length of the
   // reduction (dyn = 2); a multiple of 256 rows is readable either way
   const int* rows;
@@ -255,21 +254,19 @@ __device__ __forceinline__ Unit unit_of(int u, int m_tiles, int n_tiles, int k_s
 }
 
 // Splits of the reduction for `tiles` tiles of `k_stages` stages on `pairs`
-// pairs, at most `most`: the rounds of units (whole tiles or parts of them)
-// that the busiest pair runs, each its stages and about 6 more to fill and
-// drain.
-__host__ __device__ inline int even_splits(int tiles, int k_stages, int most, int pairs) {
-  int best = 1, best_cost = 1 << 30;
-  for (int sp = 1; sp <= most && sp <= k_stages; ++sp) {
+// pairs, at most `most` (<= 32): the rounds of units (whole tiles or parts of
+// them) that the busiest pair runs, each its stages and about 6 more to fill
+// and drain.  A lane of the calling warp looks at one number each.
+__device__ inline int even_splits(int tiles, int k_stages, int most, int pairs) {
+  const int sp = (threadIdx.x & 31) + 1;
+  int cost = INT32_MAX;
+  if (sp <= most && sp <= k_stages) {
     const int kps = (k_stages + sp - 1) / sp;
-    if ((k_stages + kps - 1) / kps != sp) continue;  // an empty last split
-    const int cost = (tiles * sp + pairs - 1) / pairs * (kps + 6);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = sp;
-    }
+    if ((k_stages + kps - 1) / kps == sp)  // no empty last split
+      cost = (tiles * sp + pairs - 1) / pairs * (kps + 6);
   }
-  return best;
+  const int least = __reduce_min_sync(0xffffffffu, cost);
+  return __ffs(__ballot_sync(0xffffffffu, cost == least));
 }
 
 template <typename T, bool AMN, bool BMN, int EPI, int TN>
@@ -353,8 +350,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
       kps = max(1, (k_stages + p.splits - 1) / p.splits);
     }
   }
-  if (EPI == E_PART && p.most_splits) {
-    splits = even_splits(m_tiles * p.n_tiles, k_stages, p.most_splits, p.pairs);
+  if (EPI == E_PART && p.splits_of) {
+    splits = *p.splits_of;
     kps = (k_stages + splits - 1) / splits;
   }
   const int units = m_tiles * p.n_tiles * splits;
@@ -843,7 +840,7 @@ cudaError_t launch_gemm_maps(const CUtensorMap& am, const CUtensorMap& bm, const
   const size_t smem = sizeof(GemmSmemFor<EPI, TN>) + 1024;
   cudaError_t err = set_max_dynamic_smem_once(kp, (int)smem);
   if (err != cudaSuccess) return err;
-  const int64_t units = (int64_t)p.m_tiles * p.n_tiles * std::max(p.splits, p.most_splits);
+  const int64_t units = (int64_t)p.m_tiles * p.n_tiles * p.splits;
   if (units > INT32_MAX / 2) return cudaErrorInvalidValue;
   const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(max_pairs(kp, smem), units));
   cudaLaunchConfig_t cfg = {};
@@ -883,26 +880,29 @@ struct Plan {
   int tn, splits;
 };
 // Modelled time of a product of `rows` x `cols` over `k_stages` stages, in
-// microseconds.  A stage of a 256-row tile costs its MMAs (0.27 us at 256
-// columns; at 128 the shared-memory reads of A bound it) or, where few
-// row tiles share a column tile, its operands' way from memory at this pair's
-// share of 6.4 TB/s; a unit costs about 1 us more to fill and drain.  Splits
-// cost the joining launch (3 us) and their partial sums' way through L2.
+// microseconds.  A stage costs an SM's way from L2, about 100 GB/s: 0.32 us for
+// the 32 KB of a 256-column tile, 0.25 us for the 24 KB of 128 columns; or, where
+// few row tiles share a column tile, its operands' way from memory at this
+// pair's share of 6.4 TB/s.  A unit costs about 3 us more to fill and drain.
+// Splits cost the joining launch (4 us) and their partial sums' way through L2.
 inline Plan plan_product(int64_t rows, int64_t cols, int k_stages, int most_tiles) {
   const int pairs = device_pairs(), mt = ceil_div(rows, TILE);
   Plan best = {TILE, 1};
   double best_cost = 1e30;
   for (int tn = TILE; tn >= 128; tn /= 2) {
     const int tiles = mt * ceil_div(cols, tn);
-    const double mma = tn == 256 ? 0.27 : 0.15;
+    const double l2 = tn == 256 ? 0.32 : 0.25;
     const double bytes = 128.0 * (std::min<int64_t>(rows, TILE) + tn) / std::min(mt, 4);
-    const double stage = std::max(mma, bytes / (6.4e6 / pairs));
+    const double stage = std::max(l2, bytes / (6.4e6 / pairs));
     for (int sp = 1; sp <= 16 && sp <= k_stages; ++sp) {
       if (sp > 1 && (tn != TILE || tiles * sp > most_tiles)) break;
       const int kps = ceil_div(k_stages, sp);
       if (ceil_div(k_stages, kps) != sp) continue;  // an empty last split
-      double cost = ceil_div((int64_t)tiles * sp, pairs) * (kps * stage + 1.0 + 0.004 * tn);
-      if (sp > 1) cost += 3.0 + 0.03 * tiles * sp;
+      const int rounds = ceil_div((int64_t)tiles * sp, pairs);
+      // a round's drain runs under the next one's stages
+      double cost = rounds * kps * stage + 2.0 + 0.004 * tn;
+      if (rounds > 1) cost += (rounds - 1) * std::max(0.0, 0.008 * tn - kps * stage);
+      if (sp > 1) cost += 4.0 + 0.015 * tiles * sp;
       if (cost < best_cost) {
         best_cost = cost;
         best = {tn, sp};
@@ -922,9 +922,7 @@ enum Finish {
 struct FinishArgs {
   const float* part;  // [split][tile][256 columns][256 rows]
   int splits, n_tiles;
-  // most_splits > 0: the splits as dense_gemm_kernel picked them for *rows
-  int most_splits, k_stages, pairs;
-  const int* rows;
+  const int* splits_of;  // device word with the splits, or null
   size_t split_stride;  // floats
   int M, N;             // rows and columns of out
   const float* residual;
@@ -936,56 +934,66 @@ struct FinishArgs {
   int32_t* dev_err;
 };
 
-// One block joins 32 rows x 64 columns: the splits' partial sums are added in
-// split order (so the result does not depend on timing), turned from
+// One block joins 32 rows x 64 columns.  Groups of eight warps take every
+// G-th split each, all their loads in flight at once, and the groups' sums are
+// added in order (so the result does not depend on timing), turned from
 // [column][row] to rows through shared memory, and finished.  Bound by the
 // partial sums' way out of L2.
+template <int FIN>
+constexpr int finish_groups() {
+  return FIN == F_SWIGLU ? 2 : 4;
+}
 template <typename T, int FIN>
-__global__ void __launch_bounds__(256) finish_kernel(FinishArgs p) {
-  __shared__ float t0[64][33];
-  __shared__ float t1[FIN == F_SWIGLU ? 64 : 1][33];
+__global__ void __launch_bounds__(256 * finish_groups<FIN>()) finish_kernel(FinishArgs p) {
+  constexpr int G = finish_groups<FIN>();
+  __shared__ float t0[G][64][33];
+  __shared__ float t1[FIN == F_SWIGLU ? G : 1][FIN == F_SWIGLU ? 64 : 1][33];
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = (threadIdx.x >> 5) & 7, grp = threadIdx.x >> 8, lane = threadIdx.x & 31;
   const int c0 = blockIdx.x * 64, row0 = blockIdx.y * 32;
   {
     const int row = row0 + lane;
     int cr = row < p.M ? row : -1;
+    const int splits = p.splits_of ? *p.splits_of : p.splits;
     if (p.row_of && cr >= 0) cr = p.row_of[row];
     const int nt = FIN == F_SWIGLU ? c0 / (TILE / 2) : c0 / TILE;
     const int col = FIN == F_SWIGLU ? c0 % (TILE / 2) : c0 % TILE;
     const float* src = p.part + ((size_t)(cr >> 8) * p.n_tiles + nt) * (size_t)TILE_FLOATS +
-                       (size_t)col * TILE + (cr & 255);
+                       (size_t)(col + warp) * TILE + (cr & 255);
     float a[8] = {}, b[8] = {};
-    int splits = p.splits;
-    if (p.most_splits)
-      splits = even_splits((*p.rows + TILE - 1) / TILE * p.n_tiles, p.k_stages, p.most_splits,
-                           p.pairs);
     if (cr >= 0) {
+      src += (size_t)grp * p.split_stride;
 #pragma unroll 4
-      for (int sp = 0; sp < splits; ++sp, src += p.split_stride) {
+      for (int sp = grp; sp < splits; sp += G, src += G * p.split_stride) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          a[i] += src[(size_t)(warp + 8 * i) * TILE];
-          if (FIN == F_SWIGLU) b[i] += src[(size_t)(warp + 8 * i + TILE / 2) * TILE];
+          a[i] += src[(size_t)(8 * i) * TILE];
+          if (FIN == F_SWIGLU) b[i] += src[(size_t)(8 * i + TILE / 2) * TILE];
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      t0[warp + 8 * i][lane] = a[i];
-      if (FIN == F_SWIGLU) t1[warp + 8 * i][lane] = b[i];
+      t0[grp][warp + 8 * i][lane] = a[i];
+      if (FIN == F_SWIGLU) t1[grp][warp + 8 * i][lane] = b[i];
     }
   }
   __syncthreads();
+  if (threadIdx.x >= 256) return;
   const int r = threadIdx.x >> 3, cj = (threadIdx.x & 7) * 8;
   const int row = row0 + r, col = c0 + cj;
   if (row >= p.M || col >= p.N) return;  // N is a multiple of 8
   float v[8], w[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    v[e] = t0[cj + e][r];
-    w[e] = FIN == F_SWIGLU ? t1[cj + e][r] : 0.0f;
+    v[e] = t0[0][cj + e][r];
+    w[e] = FIN == F_SWIGLU ? t1[0][cj + e][r] : 0.0f;
+#pragma unroll
+    for (int g = 1; g < G; ++g) {
+      v[e] += t0[g][cj + e][r];
+      if (FIN == F_SWIGLU) w[e] += t1[g][cj + e][r];
+    }
   }
   bool ovf = false;
   auto put = [&](void* base, size_t at, const float (&x)[8]) {
@@ -1040,8 +1048,8 @@ __global__ void __launch_bounds__(256) finish_kernel(FinishArgs p) {
 
 template <typename T, int FIN>
 cudaError_t launch_finish(const FinishArgs& p, cudaStream_t s) {
-  return launch_pdl(finish_kernel<T, FIN>, dim3(ceil_div(p.N, 64), ceil_div(p.M, 32)), dim3(256), 0,
-                    s, p);
+  return launch_pdl(finish_kernel<T, FIN>, dim3(ceil_div(p.N, 64), ceil_div(p.M, 32)),
+                    dim3(256 * finish_groups<FIN>()), 0, s, p);
 }
 
 }  // namespace dense

@@ -106,6 +106,7 @@ cudaError_t forward(const void* X, const void* W_gu, const void* W_d, int M, int
     a.early = 1;
     a.out = Y;
     a.residual = residual;
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + align1k((size_t)M * I * 2));
     return launch_skinny<T, false, S_STORE>({W_d, H, I, I}, h, I, M, a, s);
   }
   float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + align1k((size_t)M * I * 2));
@@ -186,6 +187,7 @@ cudaError_t backward(const void* dY, const void* X, const void* gu, const void* 
     if (dX) {
       a.early = 1;
       a.out = dX;
+      a.part = part;
       e = launch_skinny<T, true, S_STORE>({W_gu, H, I2, H}, dgu, I2, M, a, s);
       if (e) return e;
     }
@@ -233,13 +235,16 @@ using namespace moe;
 
 size_t gated_ffn_forward_workspace(int M, int H, int I) {
   const size_t h = align1k((size_t)M * I * 2);
-  if (M <= kSkinnyRows) return h;
+  if (M <= kGemvRows) return h;
+  if (M <= kSkinnyRows) return h + skinny_part_bytes(M, H, I);
   return h + std::max(part_bytes(M, 2 * (int64_t)I, H), part_bytes(M, H, I));
 }
 size_t gated_ffn_backward_workspace(int M, int H, int I) {
   const int64_t I2 = 2 * (int64_t)I;
-  const size_t part = std::max(std::max(part_bytes(M, I, H), part_bytes(M, H, I2)),
-                               std::max(part_bytes(I2, H, M), part_bytes(H, I, M)));
+  const size_t part =
+      std::max(std::max(part_bytes(I2, H, M), part_bytes(H, I, M)),
+               M <= kSkinnyRows ? skinny_part_bytes(M, H, I2)
+                                : std::max(part_bytes(M, I, H), part_bytes(M, H, I2)));
   return align1k((size_t)M * I * 2) + align1k((size_t)M * I * 4) + part;
 }
 

@@ -9,7 +9,10 @@
 // which k sits in which MMA slot, so a thread feeds the 16 consecutive bytes
 // that it loads (8 k of its row) to two MMAs as they are and loads the tokens'
 // rows in the same pattern: wide loads, no shuffles, no shared memory but for
-// the eight warps' sums at the end, which are added in warp order.
+// the eight warps' sums at the end, which are added in warp order.  Where k is
+// long and the blocks are few, a cluster of 2 to 8 blocks shares the rows along
+// k and its first block adds the others' sums, in order, through distributed
+// shared memory.
 #pragma once
 
 #include "dense_gemm.cuh"
@@ -38,6 +41,12 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ float2 lds_cluster2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
 // UP: out = h [M, rows], gu (if given) [M, 2 rows], A = W_gu [2 rows, K].
 // Otherwise out [M, rows] (+ residual), A = W_d [rows, K].  NT: groups of 8
 // tokens.  K and rows are multiples of 8.  The down form is launched right
@@ -49,6 +58,9 @@ __global__ void __launch_bounds__(32 * kGemvWarps) ffn_gemv_kernel(
     const float* __restrict__ residual, T* __restrict__ out, T* __restrict__ gu,
     int32_t* dev_err) {
   __shared__ float sums[kGemvWarps][NT][32][4];
+  __shared__ float2 joined[NT][64];
+  const int cs = (int)cluster_size(), rank = (int)cluster_rank();
+  const int row_blk = blockIdx.x / cs;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   if (UP) {
     pdl_wait();
@@ -56,7 +68,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps) ffn_gemv_kernel(
   }
   // this thread's two weight rows (clamped to a real one; the last block of
   // the down form may own 8 rows only) and its tokens' rows
-  const int r0 = UP ? blockIdx.x * 8 + g : blockIdx.x * 16 + g;
+  const int r0 = UP ? row_blk * 8 + g : row_blk * 16 + g;
   const int r1 = UP ? rows + r0 : min(r0 + 8, rows - 1);
   const T* a0p = A + (size_t)r0 * K + 8 * t;
   const T* a1p = A + (size_t)r1 * K + 8 * t;
@@ -69,14 +81,16 @@ __global__ void __launch_bounds__(32 * kGemvWarps) ffn_gemv_kernel(
   }
   float acc[NT][4] = {};
   const int chunks = (K + 31) / 32;
+  const int lo = chunks * rank / cs, hi = chunks * (rank + 1) / cs;  // this block's
+  const int kend = min(K, 32 * hi);
   const uint4 zero = make_uint4(0, 0, 0, 0);
   bool first = !UP;
-  for (int c0 = warp; c0 < chunks; c0 += kGemvWarps * kGemvUnroll) {
+  for (int c0 = lo + warp; c0 < hi; c0 += kGemvWarps * kGemvUnroll) {
     uint4 a0[kGemvUnroll], a1[kGemvUnroll];
 #pragma unroll
     for (int i = 0; i < kGemvUnroll; ++i) {
       const int k = 32 * (c0 + i * kGemvWarps);
-      const bool in = k + 8 * t < K;
+      const bool in = k + 8 * t < kend;
       a0[i] = in ? ldg_stream_u4(a0p + k) : zero;
       a1[i] = in ? ldg_stream_u4(a1p + k) : zero;
     }
@@ -88,8 +102,8 @@ __global__ void __launch_bounds__(32 * kGemvWarps) ffn_gemv_kernel(
 #pragma unroll
     for (int i = 0; i < kGemvUnroll; ++i) {
       const int k = 32 * (c0 + i * kGemvWarps);
-      if (k >= K) break;
-      const bool in = k + 8 * t < K;
+      if (k >= kend) break;
+      const bool in = k + 8 * t < kend;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const uint4 b = in && live[n] ? *reinterpret_cast<const uint4*>(xp[n] + k) : zero;
@@ -108,19 +122,44 @@ __global__ void __launch_bounds__(32 * kGemvWarps) ffn_gemv_kernel(
         make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
   __syncthreads();
   // accumulator e of lane 4 g + t is weight row g (e < 2) or g + 8, token 2 t + (e & 1)
-  bool ovf = false;
-  for (int i = threadIdx.x; i < NT * 64; i += 32 * kGemvWarps) {
+  auto add = [&](int i) {
     const int n = i >> 6, tok_l = (i >> 3) & 7, row = i & 7;
-    const int src = 4 * row + (tok_l >> 1), e = tok_l & 1, tok = 8 * n + tok_l;
-    if (tok >= M) continue;
-    float v0 = 0.0f, v1 = 0.0f;
+    const int src = 4 * row + (tok_l >> 1), e = tok_l & 1;
+    float2 v = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int w = 0; w < kGemvWarps; ++w) {
-      v0 += sums[w][n][src][e];
-      v1 += sums[w][n][src][2 + e];
+      v.x += sums[w][n][src][e];
+      v.y += sums[w][n][src][2 + e];
+    }
+    return v;
+  };
+  if (cs > 1) {
+    for (int i = threadIdx.x; i < NT * 64; i += 32 * kGemvWarps) joined[i >> 6][i & 63] = add(i);
+    cluster_sync();
+  }
+  bool ovf = false;
+  for (int i = threadIdx.x; i < NT * 64 && rank == 0; i += 32 * kGemvWarps) {
+    const int n = i >> 6, tok_l = (i >> 3) & 7, row = i & 7, tok = 8 * n + tok_l;
+    if (tok >= M) continue;
+    float v0, v1;
+    if (cs == 1) {
+      const float2 v = add(i);
+      v0 = v.x;
+      v1 = v.y;
+    } else {
+      float2 o[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        o[r] = r < cs ? lds_cluster2(cluster_addr(&joined[n][i & 63], r)) : make_float2(0.f, 0.f);
+      v0 = v1 = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        v0 += o[r].x;
+        v1 += o[r].y;
+      }
     }
     if (UP) {
-      const int j = blockIdx.x * 8 + row;
+      const int j = row_blk * 8 + row;
       const float h = v0 * sigmoid_fast(v0) * v1;
       ovf |= overflows_out<T>(h);
       out[(size_t)tok * rows + j] = from_f32<T>(h);
@@ -132,7 +171,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps) ffn_gemv_kernel(
     } else {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int j = blockIdx.x * 16 + 8 * half + row;
+        const int j = row_blk * 16 + 8 * half + row;
         if (j >= rows) continue;
         float v = half ? v1 : v0;
         if (residual) v += residual[(size_t)tok * rows + j];
@@ -141,21 +180,50 @@ __global__ void __launch_bounds__(32 * kGemvWarps) ffn_gemv_kernel(
       }
     }
   }
+  if (cs > 1) cluster_sync();  // the first block has read the others' sums
   if (ovf) set_dev_err(dev_err, MOE_DEVERR_RANGE);
+}
+
+// Blocks per row block: until one round of loads (8 warps x 8 chunks of 32 k) or
+// four blocks per SM is reached.  464 x 7712, 5 tokens: one block a row block
+// took 15 us.
+inline int gemv_cluster(int blocks, int K) {
+  int c = 1;
+  while (c < 8 && K > c * 32 * kGemvWarps * kGemvUnroll && 2 * c * blocks <= 4 * device_sm_count())
+    c *= 2;
+  return c;
+}
+
+template <typename T, int NT, bool UP>
+cudaError_t launch_gemv(const void* A, const void* X, int M, int rows, int K,
+                        const float* residual, void* out, void* gu, int32_t* dev_err,
+                        cudaStream_t s) {
+  const int blocks = UP ? rows / 8 : ceil_div(rows, 16), c = gemv_cluster(blocks, K);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks * c);
+  cfg.blockDim = dim3(32 * kGemvWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = c;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = c > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, ffn_gemv_kernel<T, NT, UP>, static_cast<const T*>(A),
+                            static_cast<const T*>(X), M, rows, K, residual, static_cast<T*>(out),
+                            static_cast<T*>(gu), dev_err);
 }
 
 template <typename T, int NT>
 cudaError_t launch_ffn_gemv(const void* X, const void* W_gu, const void* W_d, int M, int H, int I,
                             const float* residual, void* Y, void* gu, void* h, int32_t* dev_err,
                             cudaStream_t s) {
-  cudaError_t e = launch_pdl(ffn_gemv_kernel<T, NT, true>, dim3(I / 8), dim3(32 * kGemvWarps), 0, s,
-                             static_cast<const T*>(W_gu), static_cast<const T*>(X), M, I, H,
-                             static_cast<const float*>(nullptr), static_cast<T*>(h),
-                             static_cast<T*>(gu), dev_err);
-  if (e) return e;
-  return launch_pdl(ffn_gemv_kernel<T, NT, false>, dim3(ceil_div(H, 16)), dim3(32 * kGemvWarps), 0,
-                    s, static_cast<const T*>(W_d), static_cast<const T*>(h), M, H, I, residual,
-                    static_cast<T*>(Y), static_cast<T*>(nullptr), dev_err);
+  if (cudaError_t e = launch_gemv<T, NT, true>(W_gu, X, M, I, H, nullptr, h, gu, dev_err, s))
+    return e;
+  return launch_gemv<T, NT, false>(W_d, h, M, H, I, residual, Y, nullptr, dev_err, s);
 }
 
 }  // namespace dense

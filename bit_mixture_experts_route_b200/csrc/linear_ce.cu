@@ -30,6 +30,7 @@ constexpr int kPartTiles = 148;
 
 struct Meta {
   int rows;         // that count
+  int splits;       // of dX's reduction (see even_splits)
   float out_scale;  // of dl's products: max |dloss| / the unit of dl
 };
 
@@ -54,7 +55,8 @@ __global__ void __launch_bounds__(256) ce_gather_kernel(
     int* __restrict__ inv, int* __restrict__ row_of, uint4* __restrict__ Xc,
     int* __restrict__ ctarget, float* __restrict__ ctsum, float* __restrict__ clse,
     float* __restrict__ cscale, float* __restrict__ loss, float* __restrict__ lse,
-    uint4* __restrict__ dX, int32_t* dev_err) {
+    uint4* __restrict__ dX, int n_tiles, int k_stages, int most_splits, int pairs,
+    int32_t* dev_err) {
   __shared__ int s_all[8], s_before[8];
   __shared__ float s_big[8];
   pdl_wait();
@@ -107,6 +109,10 @@ __global__ void __launch_bounds__(256) ce_gather_kernel(
   if (blockIdx.x == 0 && tid == 0) {
     meta->rows = all;
     meta->out_scale = big / in_unit;
+  }
+  if (blockIdx.x == 0 && warp == 1 && most_splits > 0) {
+    const int sp = even_splits((all + TILE - 1) / TILE * n_tiles, k_stages, most_splits, pairs);
+    if (lane == 0) meta->splits = sp;
   }
   if (blockIdx.x == 0 && bad) set_dev_err(dev_err, MOE_DEVERR_BAD_INDEX);
   const int end = (all + TILE - 1) / TILE * TILE;  // of the zero rows
@@ -254,7 +260,9 @@ Space space_of(int T, int H, int V, bool backward) {
     w.pieces = ceil_div(V, w.piece);
     w.dl = take((size_t)w.rows_pad * w.piece * 2);
     w.skinny = T <= kSkinnyRows && w.pieces == 1;
-    if (!w.skinny) {
+    if (w.skinny) {
+      w.part = take(skinny_part_bytes(T, H, V));
+    } else {
       const int tiles = w.rows_pad / TILE * ceil_div(H, TILE);
       w.most_splits = std::min(16, std::max(4, kPartTiles / tiles));
       w.part = take((size_t)w.most_splits * tiles * TILE_FLOATS * 4);
@@ -281,7 +289,8 @@ cudaError_t gather(const Space& w, char* ws, const void* X, const void* W, const
                     reinterpret_cast<int*>(ws + w.ctarget), reinterpret_cast<float*>(ws + w.tsum),
                     reinterpret_cast<float*>(ws + w.clse),
                     reinterpret_cast<float*>(ws + w.cscale), loss, lse,
-                    static_cast<uint4*>(dX), dev_err);
+                    static_cast<uint4*>(dX), ceil_div(H, TILE), w.piece / GK, w.most_splits,
+                    device_pairs(), dev_err);
 }
 
 template <typename T>
@@ -386,6 +395,7 @@ cudaError_t backward(const float* dloss, const void* X, const void* W, const int
       a.out = dX;
       a.scale = &meta->out_scale;
       a.row_of = reinterpret_cast<const int*>(ws + w.row_of);
+      a.part = reinterpret_cast<float*>(ws + w.part);
       e = launch_skinny<T, true, S_STORE>({W, H, V, H}, ws + w.dl, w.piece, w.rows_pad, a, s);
       if (e) return e;
     }
@@ -429,9 +439,8 @@ cudaError_t backward(const float* dloss, const void* X, const void* W, const int
       // every piece adds to the same splits' sums, so all run as many stages:
       // a shorter last piece reads zeros behind its end
       q.k_stages = w.piece / GK;
-      q.splits = 1;
-      q.most_splits = w.most_splits;
-      q.pairs = device_pairs();
+      q.splits = w.most_splits;
+      q.splits_of = &meta->splits;
       q.rows = &meta->rows;
       q.dyn = 1;
       q.part = part;
@@ -449,10 +458,7 @@ cudaError_t backward(const float* dloss, const void* X, const void* W, const int
   if (!dX) return cudaSuccess;
   FinishArgs f = {};
   f.part = part;
-  f.most_splits = w.most_splits;
-  f.k_stages = w.piece / GK;
-  f.pairs = device_pairs();
-  f.rows = &meta->rows;
+  f.splits_of = &meta->splits;
   f.n_tiles = ht;
   f.split_stride = (size_t)mt * ht * TILE_FLOATS;
   f.M = rows;

@@ -12,7 +12,9 @@
 // sums in its shared memory and joins its share of the tokens from all CTAs of
 // the cluster through distributed shared memory, in rank order, so the result
 // does not depend on timing and nothing goes through global memory or a second
-// launch.  Persistent: a cluster walks tiles, and the tensor memory holds two
+// launch.  Where even clusters of 8 leave most SMs idle (a short row of W, a long
+// k), several clusters take a slice of k each and leave fp32 sums that a second
+// launch adds in slice order.  Persistent: a cluster walks tiles, and the tensor memory holds two
 // accumulators, so that loads and MMAs of the next tile run under the join.
 //
 // Warp roles (384 threads): warp 0 loads (TMA), warp 1 issues the MMAs and owns
@@ -44,6 +46,8 @@ struct SkinnyArgs {
   const int* live;  // device: tokens that count (<= M), or null: M
   int rows;      // columns of the result (S_SWIGLU: of h)
   int tiles, k_stages, stages, early;
+  int slices;    // of k, over clusters; S_STORE only
+  float* part;   // slices > 1: [slice][M][rows] sums
   const float* residual;
   const float* scale;
   const int* row_of;
@@ -77,11 +81,6 @@ inline int skinny_stages(int n) {
   return std::min(kSkinnyStages, room / skinny_stage(n));
 }
 
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
 __device__ __forceinline__ void mma_ss_one(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
                                            uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -143,10 +142,12 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
   tc_fence_after();
   const uint32_t tmem_base = sm.tmem_base;
 
-  // this CTA's stages of every tile, and the tiles of its cluster
-  const int k0 = (int)((int64_t)p.k_stages * rank / cs);
-  const int k1 = (int)((int64_t)p.k_stages * (rank + 1) / cs);
-  const int t0 = blockIdx.x / cs, tstep = gridDim.x / cs;
+  // this CTA's stages of every tile, and the tiles of its cluster: a cluster
+  // keeps its slice (the grid is a multiple of the slices' clusters)
+  const int slice = (blockIdx.x / cs) % p.slices, share = slice * cs + rank;
+  const int k0 = (int)((int64_t)p.k_stages * share / (cs * p.slices));
+  const int k1 = (int)((int64_t)p.k_stages * (share + 1) / (cs * p.slices));
+  const int t0 = blockIdx.x / cs / p.slices, tstep = gridDim.x / cs / p.slices;
 
   if (warp == 0) {
     // ---------------- TMA producer
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
       if constexpr (EPI == S_STORE || EPI == S_SWIGLU_BWD) {
         // what the join will read, on its way to L2 under the MMAs
         const int col = tile * CM + 4 * lane;
-        if (col < p.rows && (EPI == S_SWIGLU_BWD || p.residual))
+        if (col < p.rows && (EPI == S_SWIGLU_BWD || (p.residual && p.slices == 1)))
           for (int t = rank + cs * ew; t < tokens; t += cs * EPI_NW) {
             if (EPI == S_STORE) {
               prefetch_l2(p.residual + (size_t)t * p.rows + col);
@@ -330,7 +331,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
           const float4 v4 = sum4(t, 4 * lane);
           float v[4] = {v4.x, v4.y, v4.z, v4.w};
           if constexpr (EPI == S_STORE) {
-            if (col < p.rows) {
+            if (col < p.rows && p.slices > 1) {
+              *reinterpret_cast<float4*>(p.part + ((size_t)slice * p.M + t) * p.rows + col) = v4;
+            } else if (col < p.rows) {
               const size_t at = (size_t)(p.row_of ? p.row_of[t] : t) * p.rows + col;
               if (p.scale) {
 #pragma unroll
@@ -455,7 +458,58 @@ inline int max_clusters(const void* kern, int c) {
   return n;
 }
 
+// Adds the slices' sums: a thread takes four columns of a token.
+template <typename T>
+__global__ void __launch_bounds__(256) skinny_join_kernel(SkinnyArgs p) {
+  pdl_wait();
+  pdl_trigger();
+  const int tokens = p.live ? min(*p.live, p.M) : p.M;
+  const int t = blockIdx.y, col = 4 * (blockIdx.x * 256 + threadIdx.x);
+  if (t >= tokens || col >= p.rows) return;
+  const float* src = p.part + (size_t)t * p.rows + col;
+  const size_t step = (size_t)p.M * p.rows;
+  float4 a = *reinterpret_cast<const float4*>(src);
+#pragma unroll 8
+  for (int i = 1; i < p.slices; ++i) {
+    const float4 b = *reinterpret_cast<const float4*>(src + i * step);
+    a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+  }
+  float v[4] = {a.x, a.y, a.z, a.w};
+  const size_t at = (size_t)(p.row_of ? p.row_of[t] : t) * p.rows + col;
+  if (p.scale) {
+    const float scale = *p.scale;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] *= scale;
+  }
+  if (p.residual) {
+    const float4 r = *reinterpret_cast<const float4*>(p.residual + at);
+    v[0] += r.x; v[1] += r.y; v[2] += r.z; v[3] += r.w;
+  }
+  bool ovf = false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) ovf |= overflows_out<T>(v[e]);
+  *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at) =
+      make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
+  if (ovf) set_dev_err(p.dev_err, MOE_DEVERR_RANGE);
+}
+
+// Slices of k for W of `rows` x `k`: as many clusters of 8 as fill the device,
+// where one slice would leave half of it idle for 5 us or more (a CTA reads a
+// stage in about 0.3 us) -- the joining launch costs about 4.
+inline int skinny_slices(int64_t rows, int64_t k) {
+  const int tiles = ceil_div(rows, CM), stages = ceil_div(k, GK);
+  const int most = device_sm_count() / (8 * tiles);
+  if (most < 2) return 1;
+  const int s = std::min(most, stages / 32);  // 4 stages per CTA at least
+  return s > 1 && 0.3 * stages / 8 * (1.0 - 1.0 / s) > 5.0 ? s : 1;
+}
+inline size_t skinny_part_bytes(int M, int64_t rows, int64_t k) {
+  const int s = skinny_slices(rows, k);
+  return s > 1 ? (size_t)s * M * rows * 4 : 0;
+}
+
 // W: rows x k (S_SWIGLU: [2][rows][k]); X [M, k] with ldx elements per row.
+// S_STORE: p.part holds skinny_part_bytes.
 template <typename T, bool AMN, int EPI>
 cudaError_t launch_skinny(const Operand& w, const void* X, int64_t ldx, int x_rows, SkinnyArgs p,
                           cudaStream_t s) {
@@ -473,10 +527,10 @@ cudaError_t launch_skinny(const Operand& w, const void* X, int64_t ldx, int x_ro
           ? map_3d<T>(&wm, w.p, {w.k, w.rows, 2}, {w.ld, w.rows * w.ld}, {GK, 64, 1})
           : operand_map<T, AMN>(&wm, w, CM);
   if (!mapped || !map_2d<T>(&xm, X, x_rows, w.k, ldx, p.n)) return cudaErrorInvalidValue;
-  int best = 1;
+  p.slices = EPI == S_STORE ? skinny_slices(w.rows, w.k) : 1;
+  int best = p.slices > 1 ? 8 : 1;
   double best_cost = 1e30;
-  for (int c = 1; c <= 8 && c <= p.k_stages; c *= 2) {
-    if (EPI == S_STATS && c > 1) break;
+  for (int c = 1; c <= 8 && c <= p.k_stages && p.slices == 1; c *= 2) {
     const int fit = max_clusters(kp, c);
     // rounds of the busiest cluster, each its stages and about `fixed` more
     const double cost = (double)ceil_div(p.tiles, fit) * ((double)ceil_div(p.k_stages, c) + 5.0);
@@ -485,11 +539,10 @@ cudaError_t launch_skinny(const Operand& w, const void* X, int64_t ldx, int x_ro
       best = c;
     }
   }
-#ifdef SKINNY_C
-  best = SKINNY_C;
-#endif
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(best * std::min(p.tiles, max_clusters(kp, best)));
+  // clusters per slice
+  const int clusters = std::min(p.tiles, std::max(1, max_clusters(kp, best) / p.slices));
+  cfg.gridDim = dim3(best * p.slices * clusters);
   cfg.blockDim = dim3(GEMM_THREADS);
   cfg.dynamicSmemBytes = kSkinnySmem;
   cfg.stream = s;
@@ -502,7 +555,9 @@ cudaError_t launch_skinny(const Operand& w, const void* X, int64_t ldx, int x_ro
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, wm, xm, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, wm, xm, p);
+  if (e || p.slices == 1) return e;
+  return launch_pdl(skinny_join_kernel<T>, dim3(ceil_div(p.rows, 1024), p.M), dim3(256), 0, s, p);
 }
 
 }  // namespace dense
