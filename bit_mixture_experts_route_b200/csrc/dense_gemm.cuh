@@ -61,12 +61,16 @@ constexpr bool is_swiglu(int epi) { return epi == E_SWIGLU || epi == E_SWIGLU_BW
 constexpr int halves_of(int epi, int tn) {
   return epi == E_SWIGLU ? tn / 128 : 2;
 }
-// Bytes of staging per epilogue warp: one block of 64 columns that the warp's
-// stores take in turn (E_SWIGLU_BWD: three of 32 columns).  More would cost an
-// operand stage, and the loads' way from L2 needs them more: at 4096 x 2048 x
-// 8192, 4 stages kept the tensor cores 71 % busy, 5 stages 87 %.
+// Bytes of staging per epilogue warp: blocks of 64 columns that the warp's
+// stores take in turn, one (E_SWIGLU), two (E_STORE, E_DLOGITS, so that a short
+// reduction's tile need not wait for its store's way out) or three of 32 columns
+// (E_SWIGLU_BWD).  More would cost an operand stage, and the loads' way from L2
+// needs them: at 4096 x 2048 x 8192, 4 stages kept the tensor cores 71 % busy, 5
+// stages 87 %.
 constexpr int stg_of(int epi) {
-  return epi == E_SWIGLU_BWD ? 3 * STG / 2 : (epi == E_PART || epi == E_STATS) ? 0 : STG;
+  return epi == E_SWIGLU_BWD ? 3 * STG / 2
+         : epi == E_SWIGLU   ? STG
+         : (epi == E_PART || epi == E_STATS) ? 0 : 2 * STG;
 }
 constexpr int stg_bytes(int epi, int tn) { return 4 * halves_of(epi, tn) * stg_of(epi); }
 // As many stages as the shared memory holds beside the staging blocks.
@@ -440,8 +444,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
     bool ovf = false;
     const float scale = (EPI == E_STORE && p.scale) ? *p.scale : 1.0f;
     // 16 bytes (8 columns) of this lane's row into chunk c of the staging block
+    uint8_t* stg_now = stg;
     auto stage16 = [&](int c, uint4 v) {
-      *reinterpret_cast<uint4*>(stg + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
+      *reinterpret_cast<uint4*>(stg_now + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
     };
     auto stage32 = [&](int c, const uint32_t (&v)[32]) {  // 32 columns from chunk c on
 #pragma unroll
@@ -576,13 +581,21 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
         }
 #pragma unroll 1
         for (int blk = 0; blk < CW / 64; ++blk) {
-          stage_free();
+          // the two staging blocks alternate: this one's last store has left it
+          stg_now = stg + (blk & 1) * STG;
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+          uint32_t w64[2][32];
+          tmem_ld64(tacc + hc * CW + 64 * blk, w64[0], w64[1]);
+          if (blk == CW / 64 - 1) release();
 #pragma unroll
           for (int h2 = 0; h2 < 2; ++h2) {
             const int c = 64 * blk + 32 * h2;  // within this warp's columns
-            uint32_t v[32];
-            load32(hc * CW + c, v);
-            if (blk == CW / 64 - 1 && h2 == 1) release();
+            uint32_t(&v)[32] = w64[h2];
+            if (none) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0u;
+            }
             if (EPI == E_DLOGITS) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
@@ -622,9 +635,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
           fence_proxy_async();
           __syncwarp();
           const int col0 = w.nt * TN + hc * CW + 64 * blk;
-          if (lane == 0 && row_w < (EPI == E_DLOGITS ? p.rows_pad : p.M) && col0 < p.N) {
-            tma_store_2d(&dmap0, stg, col0, row_w);
-            bulk_commit();
+          if (lane == 0) {
+            if (row_w < (EPI == E_DLOGITS ? p.rows_pad : p.M) && col0 < p.N)
+              tma_store_2d(&dmap0, stg_now, col0, row_w);
+            bulk_commit();  // a group per turn, stored or not: the wait above counts them
           }
         }
       } else if constexpr (EPI == E_SWIGLU) {

@@ -34,61 +34,76 @@ struct Meta {
   float out_scale;  // of dl's products: max |dloss| / the unit of dl
 };
 
+// What the gathering kernels read and write, by row and by place.
+struct GatherArgs {
+  const uint4* X;
+  const uint4* W;
+  int vecs;            // 16-byte vectors of a row
+  const int* targets;
+  int rows_all, V, ignore_index;
+  const float* dloss;  // backward: with lse_in; or null
+  const float* lse_in;
+  float in_unit;
+  Meta* meta;
+  int n_tiles, k_stages, most_splits, pairs;  // of dX's reduction; most_splits 0: none
+  int* inv;
+  int* row_of;
+  uint4* Xc;
+  int* ctarget;
+  float* ctsum;
+  float* clse;
+  float* cscale;
+  float* loss;         // forward: 0 in the other rows; or null
+  float* lse;
+  uint4* dX;           // zero rows for the other rows; or null
+  int32_t* dev_err;
+};
+
 // Gathers the rows that count, in order: place among them = how many before it
 // count.  Every block counts for itself (the targets are few next to X), so
-// one launch does it all.  Slot t of a block is row t: if it counts, one warp
-// copies its X, target and gradient scale to its place and computes its
-// target's logit in fp32; if not, the slot writes a zero row behind the last
-// place, up to the end of that 256-row tile.  inv[t] = place or -1; row_of by
-// place; loss and lse (and, where given, dX) of the other rows are 0.
+// one launch does it all.  Slot t is row t: if it counts, its X, target and
+// gradient scale go to its place, with its target's logit in fp32; if not, the
+// slot writes a zero row behind the last place, up to the end of that 256-row
+// tile.  inv[t] = place or -1; row_of by place; loss and lse (and, where given,
+// dX) of the other rows are 0.
 //
 // The target's logit is computed here, not taken from the tensor cores' sums:
 // those round toward zero at every step (about 2e-6 relative at 2048 terms),
 // which in loss = lse - l[target] and in p[target] - 1 does not average out.
 // It also stands in for the tile's own sum, so that the loss of a confident
 // row stays the logarithm of a sum >= 1.
-template <typename T>
-__global__ void __launch_bounds__(256) ce_gather_kernel(
-    const uint4* __restrict__ X, const uint4* __restrict__ W, int vecs,
-    const int* __restrict__ targets, int rows_all, int V, int ignore_index, int per_block,
-    const float* __restrict__ dloss, const float* __restrict__ lse_in, float in_unit, Meta* meta,
-    int* __restrict__ inv, int* __restrict__ row_of, uint4* __restrict__ Xc,
-    int* __restrict__ ctarget, float* __restrict__ ctsum, float* __restrict__ clse,
-    float* __restrict__ cscale, float* __restrict__ loss, float* __restrict__ lse,
-    uint4* __restrict__ dX, int n_tiles, int k_stages, int most_splits, int pairs,
-    int32_t* dev_err) {
+struct Count {
+  int all, before;  // rows that count; those before `first`
+  float big;        // max |dloss|
+};
+// By the whole block of 256 threads.
+__device__ __forceinline__ Count count_rows(const GatherArgs& p, int first) {
   __shared__ int s_all[8], s_before[8];
   __shared__ float s_big[8];
-  pdl_wait();
-  pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int first = blockIdx.x * per_block;
   int all = 0, before = 0;
   float big = 0.0f;
   bool bad = false;
   auto count = [&](int t, int y) {
-    const bool real = y != ignore_index;
-    const bool keep = real && (unsigned)y < (unsigned)V;
+    const bool real = y != p.ignore_index;
+    const bool keep = real && (unsigned)y < (unsigned)p.V;
     bad |= real && !keep;
     all += keep;
     before += keep && t < first;
-    if (keep && dloss) big = fmaxf(big, fabsf(dloss[t]));
+    if (keep && p.dloss) big = fmaxf(big, fabsf(p.dloss[t]));
   };
-  const int quads = rows_all / 4;
+  const int quads = p.rows_all / 4;
 #pragma unroll 4
   for (int i = tid; i < quads; i += 256) {
-    const int4 y = reinterpret_cast<const int4*>(targets)[i];
+    const int4 y = reinterpret_cast<const int4*>(p.targets)[i];
     count(4 * i, y.x);
     count(4 * i + 1, y.y);
     count(4 * i + 2, y.z);
     count(4 * i + 3, y.w);
   }
-  if (4 * quads + tid < rows_all) count(4 * quads + tid, targets[4 * quads + tid]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
+  if (4 * quads + tid < p.rows_all) count(4 * quads + tid, p.targets[4 * quads + tid]);
+  all = __reduce_add_sync(0xffffffffu, all);
+  before = __reduce_add_sync(0xffffffffu, before);
   big = warp_max(big);
   if (lane == 0) {
     s_all[warp] = all;
@@ -96,84 +111,157 @@ __global__ void __launch_bounds__(256) ce_gather_kernel(
     s_big[warp] = big;
   }
   __syncthreads();
-  all = before = 0;
-  big = 0.0f;
+  Count c = {0, 0, 0.0f};
 #pragma unroll
   for (int w = 0; w < 8; ++w) {
-    all += s_all[w];
-    before += s_before[w];
-    big = fmaxf(big, s_big[w]);
+    c.all += s_all[w];
+    c.before += s_before[w];
+    c.big = fmaxf(c.big, s_big[w]);
   }
   // no scaling by a zero, infinite or tiny maximum
-  if (!(big >= 1e-30f && big <= 1e30f)) big = 1.0f;
+  if (!(c.big >= 1e-30f && c.big <= 1e30f)) c.big = 1.0f;
   if (blockIdx.x == 0 && tid == 0) {
-    meta->rows = all;
-    meta->out_scale = big / in_unit;
+    p.meta->rows = c.all;
+    p.meta->out_scale = c.big / p.in_unit;
   }
-  if (blockIdx.x == 0 && warp == 1 && most_splits > 0) {
-    const int sp = even_splits((all + TILE - 1) / TILE * n_tiles, k_stages, most_splits, pairs);
-    if (lane == 0) meta->splits = sp;
+  if (blockIdx.x == 0 && warp == 1 && p.most_splits > 0) {
+    const int sp =
+        even_splits((c.all + TILE - 1) / TILE * p.n_tiles, p.k_stages, p.most_splits, p.pairs);
+    if (lane == 0) p.meta->splits = sp;
   }
-  if (blockIdx.x == 0 && bad) set_dev_err(dev_err, MOE_DEVERR_BAD_INDEX);
-  const int end = (all + TILE - 1) / TILE * TILE;  // of the zero rows
-  for (int g = 0; g < per_block; g += 32) {  // 32 slots at a time
+  if (blockIdx.x == 0 && bad) set_dev_err(p.dev_err, MOE_DEVERR_BAD_INDEX);
+  return c;
+}
+template <typename T>
+__device__ __forceinline__ void dot_add(float (&d)[4], uint4 x, uint4 w) {
+  const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 a = unpack2<T>(xs[e]), b = unpack2<T>(ws[e]);
+    d[e] = fmaf(a.x, b.x, d[e]);
+    d[e] = fmaf(a.y, b.y, d[e]);
+  }
+}
+// The scalars of slot t, by one thread: place `at`, target y (keep) or none.
+__device__ __forceinline__ void gather_scalars(const GatherArgs& p, int t, int at, bool keep,
+                                               int y, float dot, float big) {
+  p.ctarget[at] = keep ? y : -1;
+  p.ctsum[at] = dot;
+  if (keep) {
+    p.inv[t] = at;
+    p.row_of[at] = t;
+  }
+  if (p.dloss) {
+    p.clse[at] = keep ? p.lse_in[t] : 0.0f;
+    p.cscale[at] = keep ? p.dloss[t] / big * p.in_unit : 0.0f;
+  }
+}
+__device__ __forceinline__ void gather_left_out(const GatherArgs& p, int t) {
+  p.inv[t] = -1;
+  if (p.loss) {
+    p.loss[t] = 0.0f;
+    p.lse[t] = 0.0f;
+  }
+}
+
+// Few rows: a block per slot, so that a row's loads are all in flight at once
+// and run under the count.  At 84 of 169 rows of 3432 the warp-per-row form
+// took 12 us.
+template <typename T>
+__global__ void __launch_bounds__(256) ce_gather_few_kernel(const GatherArgs p) {
+  __shared__ float s_dot[8];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, t = blockIdx.x;
+  const int y = t < p.rows_all ? p.targets[t] : p.ignore_index;
+  const bool keep = y != p.ignore_index && (unsigned)y < (unsigned)p.V;
+  const uint4* src = p.X + (size_t)t * p.vecs;
+  float d[4] = {};
+  constexpr int HELD = 2;  // vectors of the row that a thread keeps
+  uint4 x[HELD];
+  if (keep) {
+    const uint4* wr = p.W + (size_t)y * p.vecs;
+    uint4 w[HELD];
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) {
+      const bool in = tid + 256 * j < p.vecs;
+      x[j] = in ? src[tid + 256 * j] : make_uint4(0, 0, 0, 0);
+      w[j] = in ? wr[tid + 256 * j] : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) dot_add<T>(d, x[j], w[j]);
+    for (int i = tid + 256 * HELD; i < p.vecs; i += 256) dot_add<T>(d, src[i], wr[i]);
+  }
+  const float dot = warp_sum((d[0] + d[1]) + (d[2] + d[3]));
+  if ((tid & 31) == 0) s_dot[tid >> 5] = dot;
+  const Count c = count_rows(p, t);  // its barrier also stands behind s_dot
+  const int at = keep ? c.before : c.all + (t - c.before);
+  if (!keep && t < p.rows_all) {
+    if (tid == 0) gather_left_out(p, t);
+    if (p.dX)
+      for (int i = tid; i < p.vecs; i += 256) p.dX[(size_t)t * p.vecs + i] = make_uint4(0, 0, 0, 0);
+  }
+  if (!keep && at >= (c.all + TILE - 1) / TILE * TILE) return;
+  uint4* dst = p.Xc + (size_t)at * p.vecs;
+#pragma unroll
+  for (int j = 0; j < HELD; ++j)
+    if (tid + 256 * j < p.vecs) dst[tid + 256 * j] = keep ? x[j] : make_uint4(0, 0, 0, 0);
+  for (int i = tid + 256 * HELD; i < p.vecs; i += 256)
+    dst[i] = keep ? src[i] : make_uint4(0, 0, 0, 0);
+  if (tid == 0) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) sum += s_dot[w];
+    gather_scalars(p, t, at, keep, y, sum, c.big);
+  }
+}
+
+// Many rows: a block takes per_block slots, a warp a row at a time.
+template <typename T>
+__global__ void __launch_bounds__(256) ce_gather_kernel(const GatherArgs p, int per_block) {
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int first = blockIdx.x * per_block;
+  const Count c = count_rows(p, first);
+  int before = c.before;
+  const int end = (c.all + TILE - 1) / TILE * TILE;  // of the zero rows
+  for (int g = 0; g < per_block; g += 32) {          // 32 slots at a time
     const int t0 = first + g;
-    const int y_l = t0 + lane < rows_all && g + lane < per_block ? targets[t0 + lane] : ignore_index;
-    const unsigned kept = __ballot_sync(
-        0xffffffffu, y_l != ignore_index && (unsigned)y_l < (unsigned)V);
+    const int y_l =
+        t0 + lane < p.rows_all && g + lane < per_block ? p.targets[t0 + lane] : p.ignore_index;
+    const unsigned kept =
+        __ballot_sync(0xffffffffu, y_l != p.ignore_index && (unsigned)y_l < (unsigned)p.V);
     for (int j = warp; j < 32 && g + j < per_block; j += 8) {
       const int t = t0 + j;
       const int rank = before + __popc(kept & ((1u << j) - 1u));  // rows that count before t
       const bool keep = (kept >> j) & 1u;
       const int y = __shfl_sync(0xffffffffu, y_l, j);
-      const int at = keep ? rank : all + (t - rank);
-      if (!keep && t < rows_all) {
-        if (lane == 0) {
-          inv[t] = -1;
-          if (loss) {
-            loss[t] = 0.0f;
-            lse[t] = 0.0f;
-          }
-        }
-        if (dX)
-          for (int i = lane; i < vecs; i += 32)
-            dX[(size_t)t * vecs + i] = make_uint4(0, 0, 0, 0);
+      const int at = keep ? rank : c.all + (t - rank);
+      if (!keep && t < p.rows_all) {
+        if (lane == 0) gather_left_out(p, t);
+        if (p.dX)
+          for (int i = lane; i < p.vecs; i += 32)
+            p.dX[(size_t)t * p.vecs + i] = make_uint4(0, 0, 0, 0);
       }
       if (!keep && at >= end) continue;
-      uint4* dst = Xc + (size_t)at * vecs;
+      uint4* dst = p.Xc + (size_t)at * p.vecs;
       float dot = 0.0f;
       if (keep) {
-        const uint4* src = X + (size_t)t * vecs;
-        const uint4* wr = W + (size_t)y * vecs;
+        const uint4* src = p.X + (size_t)t * p.vecs;
+        const uint4* wr = p.W + (size_t)y * p.vecs;
         float d[4] = {};
 #pragma unroll 4
-        for (int i = lane; i < vecs; i += 32) {
+        for (int i = lane; i < p.vecs; i += 32) {
           const uint4 x = src[i], w = wr[i];
           dst[i] = x;
-          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 a = unpack2<T>(xs[e]), b = unpack2<T>(ws[e]);
-            d[e] = fmaf(a.x, b.x, d[e]);
-            d[e] = fmaf(a.y, b.y, d[e]);
-          }
+          dot_add<T>(d, x, w);
         }
         dot = warp_sum((d[0] + d[1]) + (d[2] + d[3]));
       } else {
-        for (int i = lane; i < vecs; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
+        for (int i = lane; i < p.vecs; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
       }
-      if (lane == 0) {
-        ctarget[at] = keep ? y : -1;
-        ctsum[at] = dot;
-        if (keep) {
-          inv[t] = at;
-          row_of[at] = t;
-        }
-        if (dloss) {
-          clse[at] = keep ? lse_in[t] : 0.0f;
-          cscale[at] = keep ? dloss[t] / big * in_unit : 0.0f;
-        }
-      }
+      if (lane == 0) gather_scalars(p, t, at, keep, y, dot, c.big);
     }
     before += __popc(kept);
   }
@@ -277,20 +365,38 @@ cudaError_t gather(const Space& w, char* ws, const void* X, const void* W, const
                    int rows, int H, int V, int ignore_index, const float* dloss,
                    const float* lse_in, float* loss, float* lse, void* dX, int32_t* dev_err,
                    cudaStream_t s) {
-  const float unit = std::is_same<T, __half>::value ? 32768.0f : 1.0f;
-  // rows per block: each block reads all targets, so more of them per block
-  // once the targets are many
+  GatherArgs g = {};
+  g.X = static_cast<const uint4*>(X);
+  g.W = static_cast<const uint4*>(W);
+  g.vecs = H / 8;
+  g.targets = targets;
+  g.rows_all = rows;
+  g.V = V;
+  g.ignore_index = ignore_index;
+  g.dloss = dloss;
+  g.lse_in = lse_in;
+  g.in_unit = std::is_same<T, __half>::value ? 32768.0f : 1.0f;
+  g.meta = reinterpret_cast<Meta*>(ws + w.meta);
+  g.n_tiles = ceil_div(H, TILE);
+  g.k_stages = w.piece / GK;
+  g.most_splits = w.most_splits;
+  g.pairs = device_pairs();
+  g.inv = reinterpret_cast<int*>(ws + w.inv);
+  g.row_of = reinterpret_cast<int*>(ws + w.row_of);
+  g.Xc = reinterpret_cast<uint4*>(ws + w.xc);
+  g.ctarget = reinterpret_cast<int*>(ws + w.ctarget);
+  g.ctsum = reinterpret_cast<float*>(ws + w.tsum);
+  g.clse = reinterpret_cast<float*>(ws + w.clse);
+  g.cscale = reinterpret_cast<float*>(ws + w.cscale);
+  g.loss = loss;
+  g.lse = lse;
+  g.dX = static_cast<uint4*>(dX);
+  g.dev_err = dev_err;
+  if (rows <= 1024)
+    return launch_pdl(ce_gather_few_kernel<T>, dim3(w.rows_pad), dim3(256), 0, s, g);
+  // each block reads all targets: more rows per block once the targets are many
   const int per = rows <= 8192 ? 8 : 64;
-  return launch_pdl(ce_gather_kernel<T>, dim3(w.rows_pad / per), dim3(256), 0, s,
-                    static_cast<const uint4*>(X), static_cast<const uint4*>(W), H / 8, targets,
-                    rows, V, ignore_index, per, dloss, lse_in, unit,
-                    reinterpret_cast<Meta*>(ws + w.meta), reinterpret_cast<int*>(ws + w.inv),
-                    reinterpret_cast<int*>(ws + w.row_of), reinterpret_cast<uint4*>(ws + w.xc),
-                    reinterpret_cast<int*>(ws + w.ctarget), reinterpret_cast<float*>(ws + w.tsum),
-                    reinterpret_cast<float*>(ws + w.clse),
-                    reinterpret_cast<float*>(ws + w.cscale), loss, lse,
-                    static_cast<uint4*>(dX), ceil_div(H, TILE), w.piece / GK, w.most_splits,
-                    device_pairs(), dev_err);
+  return launch_pdl(ce_gather_kernel<T>, dim3(w.rows_pad / per), dim3(256), 0, s, g, per);
 }
 
 template <typename T>

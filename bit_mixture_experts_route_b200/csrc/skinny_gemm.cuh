@@ -249,6 +249,22 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
     uint32_t bases[8];
 #pragma unroll
     for (int r = 0; r < 8; ++r) bases[r] = cluster_addr(sums, r < cs ? r : rank);
+    // this warp's tokens are t = rank + cs * (ew + 8 i), i < 16; lane i keeps what
+    // the epilogue needs to know of the i-th
+    const int t_l = rank + cs * (ew + EPI_NW * lane);
+    int tgt_l = -1, row_l = t_l;
+    float tsum_l = 0.0f, nlse_l = 0.0f, rs_l = 0.0f;
+    if (lane < 16 && t_l < joined) {
+      if (EPI == S_STATS || EPI == S_DLOGITS) {
+        tgt_l = p.targets[t_l];
+        tsum_l = p.target_sum[t_l];
+      }
+      if (EPI == S_DLOGITS) {
+        nlse_l = -p.lse[t_l] * kLog2e;
+        rs_l = p.row_scale[t_l];
+      }
+      if (EPI == S_STORE && p.row_of && p.slices == 1) row_l = p.row_of[t_l];
+    }
     for (int tile = t0; tile < p.tiles && tokens > 0; tile += tstep, ++lt) {
       const int acc = lt & 1;
       if constexpr (EPI == S_STORE || EPI == S_SWIGLU_BWD) {
@@ -300,7 +316,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
         return a;
       };
 #pragma unroll 4
-      for (int t = rank + cs * ew; t < joined; t += cs * EPI_NW) {
+      for (int i = 0; i < 16; ++i) {
+        const int t = rank + cs * (ew + EPI_NW * i);
+        if (t >= joined) break;
         if constexpr (EPI == S_SWIGLU) {
           // lanes 0-15 hold gate columns 4 lane .., lanes 16-31 the same up columns
           const float4 v = sum4(t, 4 * lane);
@@ -331,10 +349,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
           const float4 v4 = sum4(t, 4 * lane);
           float v[4] = {v4.x, v4.y, v4.z, v4.w};
           if constexpr (EPI == S_STORE) {
+            const int row = __shfl_sync(0xffffffffu, row_l, i);
             if (col < p.rows && p.slices > 1) {
               *reinterpret_cast<float4*>(p.part + ((size_t)slice * p.M + t) * p.rows + col) = v4;
             } else if (col < p.rows) {
-              const size_t at = (size_t)(p.row_of ? p.row_of[t] : t) * p.rows + col;
+              const size_t at = (size_t)row * p.rows + col;
               if (p.scale) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] *= scale;
@@ -375,10 +394,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
                   make_uint2(pack2<T>(du[0], du[1]), pack2<T>(du[2], du[3]));
             }
           } else if constexpr (EPI == S_STATS) {
-            const int tgt = p.targets[t] - col;
+            const int tgt = __shfl_sync(0xffffffffu, tgt_l, i) - col;
+            const float tsum = __shfl_sync(0xffffffffu, tsum_l, i);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              if (tgt == e) v[e] = p.target_sum[t];
+              if (tgt == e) v[e] = tsum;
               if (col + e >= p.rows) v[e] = -INFINITY;
             }
             const float m = warp_max(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
@@ -388,12 +408,14 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
                                       exp2_approx((v[3] - m) * kLog2e)));
             if (lane == 0) p.stats[(size_t)tile * p.rows_pad + t] = make_float2(m, s);
           } else {  // S_DLOGITS
-            const float nlse = -p.lse[t] * kLog2e, rs = p.row_scale[t];
-            const int tgt = p.targets[t] - col;
+            const float nlse = __shfl_sync(0xffffffffu, nlse_l, i);
+            const float rs = __shfl_sync(0xffffffffu, rs_l, i);
+            const float tsum = __shfl_sync(0xffffffffu, tsum_l, i);
+            const int tgt = __shfl_sync(0xffffffffu, tgt_l, i) - col;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               float x = exp2_approx(fmaf(v[e], kLog2e, nlse));
-              if (tgt == e) x = exp2_approx(fmaf(p.target_sum[t], kLog2e, nlse)) - 1.0f;
+              if (tgt == e) x = exp2_approx(fmaf(tsum, kLog2e, nlse)) - 1.0f;
               v[e] = x * rs;
             }
             // rows of out are p.ld >= 128 tiles long: the last tile's end is theirs too
