@@ -32,6 +32,7 @@ struct Meta {
   int rows;         // that count
   int splits;       // of dX's reduction (see even_splits)
   float out_scale;  // of dl's products: max |dloss| / the unit of dl
+  int arrived[EPI_NW * 8];  // see SkinnyArgs, 0 from the gathering launch on
 };
 
 // What the gathering kernels read and write, by row and by place.
@@ -124,6 +125,7 @@ __device__ __forceinline__ Count count_rows(const GatherArgs& p, int first) {
     p.meta->rows = c.all;
     p.meta->out_scale = c.big / p.in_unit;
   }
+  if (blockIdx.x == 0 && tid < EPI_NW * 8) p.meta->arrived[tid] = 0;
   if (blockIdx.x == 0 && warp == 1 && p.most_splits > 0) {
     const int sp =
         even_splits((c.all + TILE - 1) / TILE * p.n_tiles, p.k_stages, p.most_splits, p.pairs);
@@ -337,7 +339,8 @@ Space space_of(int T, int H, int V, bool backward) {
   w.xc = take((size_t)w.rows_pad * H * 2);
   if (!backward) {
     w.skinny = T <= kSkinnyRows;
-    w.stats = take((size_t)2 * ceil_div(V, TILE) * w.rows_pad * sizeof(float2));
+    w.stats = take(w.skinny ? skinny_stats_bytes(T, V)
+                            : (size_t)2 * ceil_div(V, TILE) * w.rows_pad * sizeof(float2));
   } else {
     w.clse = take((size_t)w.rows_pad * 4);
     w.cscale = take((size_t)w.rows_pad * 4);
@@ -392,7 +395,7 @@ cudaError_t gather(const Space& w, char* ws, const void* X, const void* W, const
   g.lse = lse;
   g.dX = static_cast<uint4*>(dX);
   g.dev_err = dev_err;
-  if (rows <= 1024)
+  if (rows <= 2048)
     return launch_pdl(ce_gather_few_kernel<T>, dim3(w.rows_pad), dim3(256), 0, s, g);
   // each block reads all targets: more rows per block once the targets are many
   const int per = rows <= 8192 ? 8 : 64;
@@ -407,48 +410,48 @@ cudaError_t forward(const void* X, const void* W, const int* targets, int rows, 
   cudaError_t e = gather<T>(w, ws, X, W, targets, rows, H, V, ignore_index, nullptr, nullptr,
                             loss, lse, nullptr, dev_err, s);
   if (e) return e;
-  const Meta* meta = reinterpret_cast<const Meta*>(ws + w.meta);
+  Meta* meta = reinterpret_cast<Meta*>(ws + w.meta);
   float2* stats = reinterpret_cast<float2*>(ws + w.stats);
   const float* tsum = reinterpret_cast<const float*>(ws + w.tsum);
   const int* ctarget = reinterpret_cast<const int*>(ws + w.ctarget);
-  int pieces;  // of a row's statistics
+  const int* row_of = reinterpret_cast<const int*>(ws + w.row_of);
   if (w.skinny) {
     SkinnyArgs a = {};
     a.M = rows;
     a.live = &meta->rows;
     a.early = 1;
     a.stats = stats;
-    a.rows_pad = w.rows_pad;
+    a.arrived = meta->arrived;
     a.target_sum = tsum;
     a.targets = ctarget;
+    a.row_of = row_of;
+    a.loss = loss;
+    a.lse_out = lse;
     a.dev_err = dev_err;
-    pieces = ceil_div(V, CM);
-    e = launch_skinny<T, false, S_STATS>({W, V, H, H}, ws + w.xc, H, w.rows_pad, a, s);
-  } else {
-    GemmArgs p = {};
-    p.N = V;
-    p.M = rows;
-    p.m_tiles = w.rows_pad / TILE;
-    p.n_tiles = ceil_div(V, TILE);
-    p.k_stages = p.kps = ceil_div(H, GK);
-    p.splits = 1;
-    p.rows = &meta->rows;
-    p.dyn = 1;
-    p.stats = stats;
-    p.target_sum = tsum;
-    p.targets = ctarget;
-    p.rows_pad = w.rows_pad;
-    p.dev_err = dev_err;
-    pieces = 2 * p.n_tiles;
-    CUtensorMap am, bm;
-    if (!map_2d<T>(&am, ws + w.xc, w.rows_pad, H, H, CM) || !map_2d<T>(&bm, W, V, H, H, CM))
-      return cudaErrorInvalidValue;
-    e = launch_gemm_maps<T, false, false, E_STATS, 256>(am, bm, am, am, p, s);
+    return launch_skinny<T, false, S_STATS>({W, V, H, H}, ws + w.xc, H, w.rows_pad, a, s);
   }
+  GemmArgs p = {};
+  p.N = V;
+  p.M = rows;
+  p.m_tiles = w.rows_pad / TILE;
+  p.n_tiles = ceil_div(V, TILE);
+  p.k_stages = p.kps = ceil_div(H, GK);
+  p.splits = 1;
+  p.rows = &meta->rows;
+  p.dyn = 1;
+  p.stats = stats;
+  p.target_sum = tsum;
+  p.targets = ctarget;
+  p.rows_pad = w.rows_pad;
+  p.dev_err = dev_err;
+  CUtensorMap am, bm;
+  if (!map_2d<T>(&am, ws + w.xc, w.rows_pad, H, H, CM) || !map_2d<T>(&bm, W, V, H, H, CM))
+    return cudaErrorInvalidValue;
+  e = launch_gemm_maps<T, false, false, E_STATS, 256>(am, bm, am, am, p, s);
   if (e) return e;
   return launch_pdl(ce_join_kernel, dim3(w.rows_pad / 32), dim3(32 * kJoinWarps), 0, s,
-                    static_cast<const float2*>(stats), pieces, w.rows_pad, tsum, meta,
-                    reinterpret_cast<const int*>(ws + w.row_of), loss, lse);
+                    static_cast<const float2*>(stats), 2 * ceil_div(V, TILE), w.rows_pad, tsum,
+                    static_cast<const Meta*>(meta), row_of, loss, lse);
 }
 
 // Rows [v0, v0 + vn) of dW = dl^T X, from the first `reach` rows of dl.

@@ -36,7 +36,7 @@ enum SkinnyEpilogue {
   S_STORE,       // out[row_of[t] or t] = 16-bit (sum * *scale + residual)
   S_SWIGLU,      // tile = 64 gate rows, 64 up rows: out = h, out1 = gate | up (if given)
   S_SWIGLU_BWD,  // sums are dh: out = h, out1 = dgate | dup, from gu
-  S_STATS,       // per token and tile: maximum and sum of exponentials
+  S_STATS,       // per token: loss and lse of the softmax over the columns
   S_DLOGITS,     // out = (exp(sum - lse) - [column is the target]) * row scale
 };
 
@@ -55,8 +55,14 @@ struct SkinnyArgs {
   void* out;
   void* out1;
   int ld;        // S_DLOGITS: elements per row of out
-  float2* stats; // [tile][rows_pad]
-  int rows_pad;
+  // S_STATS: a cluster keeps the running maximum and sum of its tiles and leaves
+  // them in stats [cluster][M]; per subset of tokens (that of one warp in every
+  // cluster) the last cluster to arrive adds them in order.  arrived: a zeroed
+  // word per subset
+  float2* stats;
+  int* arrived;
+  float* loss;
+  float* lse_out;
   const float* target_sum;
   const int* targets;
   const float* lse;
@@ -97,6 +103,43 @@ __device__ __forceinline__ float4 lds_cluster4(uint32_t a) {
                : "r"(a)
                : "memory");
   return v;
+}
+
+// S_STATS, one warp: leaves its tokens' maximum and sum (lane i's token's m, s);
+// the last cluster's warp of this subset joins all clusters' and writes.
+__device__ __forceinline__ void stats_join(const SkinnyArgs& p, int tokens, int cluster,
+                                           int clusters, int rank, int cs, int ew, int lane,
+                                           float m, float s) {
+  const int t_l = rank + cs * (ew + EPI_NW * lane);
+  if (lane < 16 && t_l < tokens) p.stats[(size_t)cluster * p.M + t_l] = make_float2(m, s);
+  __threadfence();
+  __syncwarp();
+  int before = 0;
+  if (lane == 0) before = atomicAdd(&p.arrived[rank * EPI_NW + ew], 1);
+  if (__shfl_sync(0xffffffffu, before, 0) != clusters - 1) return;
+  __threadfence();
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) {
+    const int t = rank + cs * (ew + EPI_NW * i);
+    if (t >= tokens) break;
+    m = -INFINITY;
+    s = 0.0f;
+    for (int c = lane; c < clusters; c += 32) {
+      const float2 o = __ldcg(&p.stats[(size_t)c * p.M + t]);
+      const float mn = fmaxf(m, o.x);
+      s = (m == mn ? s : s * exp2_approx((m - mn) * kLog2e)) +
+          (o.x == mn ? o.y : o.y * exp2_approx((o.x - mn) * kLog2e));
+      m = mn;
+    }
+    const float top = warp_max(m);
+    const float sum = warp_sum(s == 0.0f ? 0.0f : s * exp2_approx((m - top) * kLog2e));
+    if (lane == 0) {
+      const float ls = logf(sum);
+      const int row = p.row_of[t];
+      p.loss[row] = (top - p.target_sum[t]) + ls;  // lse - target would lose lse's rounding
+      p.lse_out[row] = top + ls;
+    }
+  }
 }
 
 template <typename T, bool AMN, int EPI>
@@ -265,6 +308,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
       }
       if (EPI == S_STORE && p.row_of && p.slices == 1) row_l = p.row_of[t_l];
     }
+    float run_m = -INFINITY, run_s = 0.0f;  // S_STATS: lane i's token's
+    bool done = true;
     for (int tile = t0; tile < p.tiles && tokens > 0; tile += tstep, ++lt) {
       const int acc = lt & 1;
       if constexpr (EPI == S_STORE || EPI == S_SWIGLU_BWD) {
@@ -281,6 +326,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
             }
           }
       }
+      done = false;
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.acc_full[acc], (lt >> 1) & 1, sm, p.dev_err)))
         break;
       tc_fence_after();
@@ -406,7 +452,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
                                       exp2_approx((v[1] - m) * kLog2e)) +
                                      (exp2_approx((v[2] - m) * kLog2e) +
                                       exp2_approx((v[3] - m) * kLog2e)));
-            if (lane == 0) p.stats[(size_t)tile * p.rows_pad + t] = make_float2(m, s);
+            if (lane == i) {
+              const float mn = fmaxf(run_m, m);
+              run_s = run_s * exp2_approx((run_m - mn) * kLog2e) + s * exp2_approx((m - mn) * kLog2e);
+              run_m = mn;
+            }
           } else {  // S_DLOGITS
             const float nlse = __shfl_sync(0xffffffffu, nlse_l, i);
             const float rs = __shfl_sync(0xffffffffu, rs_l, i);
@@ -424,6 +474,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
           }
         }
       }
+      done = true;
       if (tile + tstep >= p.tiles) break;  // nobody waits for the last tile's
       __syncwarp();
       if (cs == 1) {
@@ -431,6 +482,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
       } else if (lane < cs) {
         mbar_arrive_remote(cluster_addr(&sm.taken, lane));
       }
+    }
+    if constexpr (EPI == S_STATS) {
+      // (after a wait that ran out, done is false in the whole warp and the error word set)
+      if (done && rank + cs * ew < tokens)
+        stats_join(p, tokens, t0, tstep, rank, cs, ew, lane, run_m, run_s);
     }
     __syncwarp();
     if (__any_sync(0xffffffffu, ovf) && lane == 0) set_dev_err(p.dev_err, MOE_DEVERR_RANGE);
@@ -528,6 +584,10 @@ inline int skinny_slices(int64_t rows, int64_t k) {
 inline size_t skinny_part_bytes(int M, int64_t rows, int64_t k) {
   const int s = skinny_slices(rows, k);
   return s > 1 ? (size_t)s * M * rows * 4 : 0;
+}
+
+inline size_t skinny_stats_bytes(int M, int64_t rows) {
+  return (size_t)std::min(ceil_div(rows, CM), device_sm_count()) * M * sizeof(float2);
 }
 
 // W: rows x k (S_SWIGLU: [2][rows][k]); X [M, k] with ldx elements per row.
