@@ -49,6 +49,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // What the epilogue does with the sums.
 enum Epilogue {
   E_STORE,       // D0 = 16-bit (sum * *scale + residual)
+  E_STORE2,      // E_STORE of two products with the same k, one unit list
   E_PART,        // partial sums to the workspace, [tile][column][row] fp32
   E_SWIGLU,      // columns are gate [0,128) | up [128,256): D0 = h, D1 = gate | up
   E_SWIGLU_BWD,  // sums are dh: D0 = h, D1 = dgate | dup, from gu
@@ -108,6 +109,15 @@ struct GemmArgs {
   int rows_pad;
   int32_t* dev_err;
 };
+
+// The second product of E_STORE2.
+struct alignas(64) SecondProduct {
+  CUtensorMap a, b, d;
+  int N, M, m_tiles, n_tiles;
+};
+struct NoProduct {};
+template <int EPI>
+using SecondFor = typename std::conditional<EPI == E_STORE2, SecondProduct, NoProduct>::type;
 
 template <int NS, int SB, int NW, int NSTG>
 struct __align__(8) GemmSmem {
@@ -277,9 +287,10 @@ template <typename T, bool AMN, bool BMN, int EPI, int TN>
 __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
     const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
     const __grid_constant__ CUtensorMap dmap0, const __grid_constant__ CUtensorMap dmap1,
-    const __grid_constant__ GemmArgs p) {
+    const __grid_constant__ GemmArgs p, const __grid_constant__ SecondFor<EPI> second) {
   extern __shared__ uint8_t smem_raw[];
   static_assert(EPI != E_PART || TN == TILE, "partial sums are whole 256 x 256 tiles");
+  static_assert(EPI != E_STORE2 || (AMN && BMN), "made for weight gradients");
   constexpr int NS = stages_of(EPI, TN), STAGE = stage_bytes(TN), BROWS = TN / 2;
   constexpr int HALVES = halves_of(EPI, TN);
   using Smem = GemmSmemFor<EPI, TN>;
@@ -318,28 +329,37 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
   const int u0 = blockIdx.x >> 1, ustep = gridDim.x >> 1;
   constexpr int NCOLS = EPI == E_SWIGLU ? TN / 2 : TN;  // columns of one tile
   const bool gate_up = EPI == E_SWIGLU || (EPI == E_PART && p.gate_up);
-  auto load_b = [&](int s, const Unit& w, int k) {
+  // E_STORE2: units from `units1` on are the second product's
+  const int units1 = EPI == E_STORE2 ? p.m_tiles * p.n_tiles : INT32_MAX;
+  auto unit_at = [&](int u, int m_tiles, int k_stages, int kps) {
+    if constexpr (EPI == E_STORE2)
+      if (u >= units1)
+        return unit_of(u - units1, second.m_tiles, second.n_tiles, k_stages, kps);
+    return unit_of(u, m_tiles, p.n_tiles, k_stages, kps);
+  };
+  auto load_b = [&](int s, const Unit& w, int k, const CUtensorMap* bmap) {
     uint8_t* b = sm.ab[s] + OPERAND;
     const uint32_t bar = cluster_addr(&sm.full[s], 0);
     const int brow = gate_up ? w.nt * BROWS : w.nt * TN + rank * BROWS;
     if (gate_up) {  // gate rows in the leader, up rows in its peer
-      tma_load_3d_pair(b, &bmap, bar, k * GK, brow, rank);
+      tma_load_3d_pair(b, bmap, bar, k * GK, brow, rank);
     } else if (BMN) {
-      tma_load_2d_pair(b, &bmap, bar, brow, k * GK);
-      if (BROWS > 64) tma_load_2d_pair(b + OPERAND / 2, &bmap, bar, brow + 64, k * GK);
+      tma_load_2d_pair(b, bmap, bar, brow, k * GK);
+      if (BROWS > 64) tma_load_2d_pair(b + OPERAND / 2, bmap, bar, brow + 64, k * GK);
     } else {
-      tma_load_2d_pair(b, &bmap, bar, k * GK, brow);
+      tma_load_2d_pair(b, bmap, bar, k * GK, brow);
     }
   };
   // the first unit's first stages: their slots are free from the start, and
-  // what the kernel before writes is not B (the host sets early without dyn)
+  // what the kernel before writes is not B (the host sets early without dyn, and
+  // for the first product)
   int early = 0;
   if (p.early && warp == 0 && lane == 0 && u0 < p.m_tiles * p.n_tiles * p.splits) {
     const Unit w = unit_of(u0, p.m_tiles, p.n_tiles, p.k_stages, p.kps);
     early = min(NS, w.k1 - w.k0);
     for (int i = 0; i < early; ++i) {
       if (leader) mbar_arrive_expect_tx(&sm.full[i], 2 * STAGE);
-      load_b(i, w, w.k0 + i);
+      load_b(i, w, w.k0 + i, &bmap);
     }
   }
   pdl_wait();
@@ -358,7 +378,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
     splits = *p.splits_of;
     kps = (k_stages + splits - 1) / splits;
   }
-  const int units = m_tiles * p.n_tiles * splits;
+  int units = m_tiles * p.n_tiles * splits;
+  if constexpr (EPI == E_STORE2) units += second.m_tiles * second.n_tiles;
 
   if (warp == 0) {
     // ---------------- TMA producer
@@ -367,7 +388,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
       uint32_t ph = 0;
       bool ok = true;
       for (int u = u0; u < units && ok; u += ustep) {
-        const Unit w = unit_of(u, m_tiles, p.n_tiles, k_stages, kps);
+        const Unit w = unit_at(u, m_tiles, k_stages, kps);
+        const CUtensorMap *am = &amap, *bm = &bmap;
+        if constexpr (EPI == E_STORE2)
+          if (u >= units1) {
+            am = &second.a;
+            bm = &second.b;
+          }
         const int arow = w.mt * TILE + rank * CM;
         for (int k = w.k0; k < w.k1; ++k) {
           const bool has_b = early > 0;  // B is on its way already
@@ -380,12 +407,12 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
           const uint32_t bar = cluster_addr(&sm.full[s], 0);
           uint8_t* a = sm.ab[s];
           if (AMN) {
-            tma_load_2d_pair(a, &amap, bar, arow, k * GK);
-            tma_load_2d_pair(a + OPERAND / 2, &amap, bar, arow + 64, k * GK);
+            tma_load_2d_pair(a, am, bar, arow, k * GK);
+            tma_load_2d_pair(a + OPERAND / 2, am, bar, arow + 64, k * GK);
           } else {
-            tma_load_2d_pair(a, &amap, bar, k * GK, arow);
+            tma_load_2d_pair(a, am, bar, k * GK, arow);
           }
-          if (!has_b) load_b(s, w, k);
+          if (!has_b) load_b(s, w, k, bm);
           ++issued;
           if (++s == NS) { s = 0; ph ^= 1; }
         }
@@ -410,7 +437,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
       uint32_t ph = 0;
       bool ok = true;
       for (int u = u0; u < units && ok; u += ustep, ++lt) {
-        const Unit w = unit_of(u, m_tiles, p.n_tiles, k_stages, kps);
+        const Unit w = unit_at(u, m_tiles, k_stages, kps);
         const int acc = lt & 1;
         if (!(ok = mbar_poll(&sm.acc_empty[acc], ((lt >> 1) & 1) ^ 1, sm, p.dev_err))) break;
         tc_fence_after();
@@ -483,7 +510,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
     // chunk c (16 bytes) of row r in a 64-byte-swizzled block
     auto at64 = [](int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); };
     for (int u = u0; u < units; u += ustep, ++lt) {
-      const Unit w = unit_of(u, m_tiles, p.n_tiles, k_stages, kps);
+      const Unit w = unit_at(u, m_tiles, k_stages, kps);
       const int acc = lt & 1;
       const int row = w.mt * TILE + rank * CM + 32 * q + lane;  // this lane's row of D
       const int row_w = row - lane;                             // the warp's first
@@ -570,7 +597,15 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
           m = mn;
         }
         p.stats[(size_t)(HALVES * w.nt + hc) * p.rows_pad + row] = make_float2(m, s);
-      } else if constexpr (EPI == E_STORE || EPI == E_DLOGITS) {
+      } else if constexpr (EPI == E_STORE || EPI == E_STORE2 || EPI == E_DLOGITS) {
+        int cols = p.N, rows_end = EPI == E_DLOGITS ? p.rows_pad : p.M;
+        const CUtensorMap* dm = &dmap0;
+        if constexpr (EPI == E_STORE2)
+          if (u >= units1) {
+            cols = second.N;
+            rows_end = second.M;
+            dm = &second.d;
+          }
         float nlse = 0.f, rs = 0.f, tl = 0.f;
         int tgt = -1;
         if (EPI == E_DLOGITS) {
@@ -636,8 +671,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
           __syncwarp();
           const int col0 = w.nt * TN + hc * CW + 64 * blk;
           if (lane == 0) {
-            if (row_w < (EPI == E_DLOGITS ? p.rows_pad : p.M) && col0 < p.N)
-              tma_store_2d(&dmap0, stg_now, col0, row_w);
+            if (row_w < rows_end && col0 < cols) tma_store_2d(dm, stg_now, col0, row_w);
             bulk_commit();  // a group per turn, stored or not: the wait above counts them
           }
         }
@@ -848,13 +882,15 @@ inline int max_pairs(const void* kern, size_t smem) {
 
 template <typename T, bool AMN, bool BMN, int EPI, int TN>
 cudaError_t launch_gemm_maps(const CUtensorMap& am, const CUtensorMap& bm, const CUtensorMap& d0,
-                             const CUtensorMap& d1, const GemmArgs& p, cudaStream_t s) {
+                             const CUtensorMap& d1, const GemmArgs& p, cudaStream_t s,
+                             const SecondFor<EPI>& second = {}) {
   auto kern = dense_gemm_kernel<T, AMN, BMN, EPI, TN>;
   const void* kp = reinterpret_cast<const void*>(kern);
   const size_t smem = sizeof(GemmSmemFor<EPI, TN>) + 1024;
   cudaError_t err = set_max_dynamic_smem_once(kp, (int)smem);
   if (err != cudaSuccess) return err;
-  const int64_t units = (int64_t)p.m_tiles * p.n_tiles * p.splits;
+  int64_t units = (int64_t)p.m_tiles * p.n_tiles * p.splits;
+  if constexpr (EPI == E_STORE2) units += (int64_t)second.m_tiles * second.n_tiles;
   if (units > INT32_MAX / 2) return cudaErrorInvalidValue;
   const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(max_pairs(kp, smem), units));
   cudaLaunchConfig_t cfg = {};
@@ -871,7 +907,7 @@ cudaError_t launch_gemm_maps(const CUtensorMap& am, const CUtensorMap& bm, const
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, am, bm, d0, d1, p);
+  return cudaLaunchKernelEx(&cfg, kern, am, bm, d0, d1, p, second);
 }
 
 // The GEMM on two plain operands; d0 / d1 are the epilogue's output maps.

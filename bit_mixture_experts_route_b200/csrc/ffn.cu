@@ -145,6 +145,31 @@ cudaError_t forward(const void* X, const void* W_gu, const void* W_d, int M, int
   return product<T, false, false>({h, M, I, I}, {W_d, H, I, I}, Y, residual, part, true, dev_err, s);
 }
 
+template <typename T, int TN>
+cudaError_t both_gradients(const void* dY, const void* X, const void* h, const void* dgu, int M,
+                           int H, int I, void* dW_gu, void* dW_d, int32_t* dev_err,
+                           cudaStream_t s) {
+  const int64_t I2 = 2 * (int64_t)I;
+  GemmArgs p = {};
+  p.N = H;
+  p.M = (int)I2;
+  p.early = 1;
+  p.dev_err = dev_err;
+  set_plan(p, I2, H, M, {TN, 1});
+  SecondProduct q = {};
+  q.N = I;
+  q.M = H;
+  q.m_tiles = ceil_div(H, TILE);
+  q.n_tiles = ceil_div(I, TN);
+  CUtensorMap am, bm, dm;
+  if (!operand_map<T, true>(&am, {dgu, I2, M, I2}, CM) ||
+      !operand_map<T, true>(&bm, {X, H, M, H}, CM) || !map_2d<T>(&dm, dW_gu, I2, H, H, 32) ||
+      !operand_map<T, true>(&q.a, {dY, H, M, H}, CM) ||
+      !operand_map<T, true>(&q.b, {h, I, M, I}, CM) || !map_2d<T>(&q.d, dW_d, H, I, I, 32))
+    return cudaErrorInvalidValue;
+  return launch_gemm_maps<T, true, true, E_STORE2, TN>(am, bm, dm, dm, p, s, q);
+}
+
 // dW_gu = dgu^T X, dW_d = dY^T h; either may be null.
 template <typename T>
 cudaError_t weight_gradients(const void* dY, const void* X, const void* h, const void* dgu, int M,
@@ -152,6 +177,17 @@ cudaError_t weight_gradients(const void* dY, const void* X, const void* h, const
                              cudaStream_t s) {
   const int64_t I2 = 2 * (int64_t)I;
   cudaError_t e;
+  if (dW_gu && dW_d && plan_of(I2, H, M).splits == 1 && plan_of(H, I, M).splits == 1) {
+    // both in one launch: their tiles share the rounds, and a launch's start and
+    // end cost about 5 us
+    auto tiles = [&](int tn) {
+      return ceil_div(I2, TILE) * ceil_div(H, tn) + ceil_div(H, TILE) * ceil_div(I, tn);
+    };
+    // tiles of 128 columns where one round takes them all
+    if (tiles(128) <= device_pairs())
+      return both_gradients<T, 128>(dY, X, h, dgu, M, H, I, dW_gu, dW_d, dev_err, s);
+    return both_gradients<T, 256>(dY, X, h, dgu, M, H, I, dW_gu, dW_d, dev_err, s);
+  }
   if (dW_gu) {
     e = product<T, true, true>({dgu, I2, M, I2}, {X, H, M, H}, dW_gu, nullptr, part, true,
                                dev_err, s);

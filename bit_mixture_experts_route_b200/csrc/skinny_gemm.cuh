@@ -56,7 +56,7 @@ struct SkinnyArgs {
   void* out1;
   int ld;        // S_DLOGITS: elements per row of out
   // S_STATS: a cluster keeps the running maximum and sum of its tiles and leaves
-  // them in stats [cluster][M]; per subset of tokens (that of one warp in every
+  // them in stats [M][clusters]; per subset of tokens (that of one warp in every
   // cluster) the last cluster to arrive adds them in order.  arrived: a zeroed
   // word per subset
   float2* stats;
@@ -109,36 +109,62 @@ __device__ __forceinline__ float4 lds_cluster4(uint32_t a) {
 // the last cluster's warp of this subset joins all clusters' and writes.
 __device__ __forceinline__ void stats_join(const SkinnyArgs& p, int tokens, int cluster,
                                            int clusters, int rank, int cs, int ew, int lane,
-                                           float m, float s) {
+                                           float m, float s, int row_l, float tsum_l) {
   const int t_l = rank + cs * (ew + EPI_NW * lane);
-  if (lane < 16 && t_l < tokens) p.stats[(size_t)cluster * p.M + t_l] = make_float2(m, s);
+  if (lane < 16 && t_l < tokens) p.stats[(size_t)t_l * clusters + cluster] = make_float2(m, s);
   __threadfence();
   __syncwarp();
   int before = 0;
   if (lane == 0) before = atomicAdd(&p.arrived[rank * EPI_NW + ew], 1);
   if (__shfl_sync(0xffffffffu, before, 0) != clusters - 1) return;
   __threadfence();
-#pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const int t = rank + cs * (ew + EPI_NW * i);
-    if (t >= tokens) break;
-    m = -INFINITY;
-    s = 0.0f;
-    for (int c = lane; c < clusters; c += 32) {
-      const float2 o = __ldcg(&p.stats[(size_t)c * p.M + t]);
-      const float mn = fmaxf(m, o.x);
-      s = (m == mn ? s : s * exp2_approx((m - mn) * kLog2e)) +
-          (o.x == mn ? o.y : o.y * exp2_approx((o.x - mn) * kLog2e));
-      m = mn;
+  float top_l = 0.0f, sum_l = 1.0f;  // lane i's token's
+  constexpr int G = 4, J = 5;        // tokens and, by 32, clusters whose loads are in flight
+  for (int i0 = 0; i0 < 16 && rank + cs * (ew + EPI_NW * i0) < tokens; i0 += G) {
+    float mg[G], sg[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      mg[g] = -INFINITY;
+      sg[g] = 0.0f;
     }
-    const float top = warp_max(m);
-    const float sum = warp_sum(s == 0.0f ? 0.0f : s * exp2_approx((m - top) * kLog2e));
-    if (lane == 0) {
-      const float ls = logf(sum);
-      const int row = p.row_of[t];
-      p.loss[row] = (top - p.target_sum[t]) + ls;  // lse - target would lose lse's rounding
-      p.lse_out[row] = top + ls;
+    for (int c0 = lane; c0 < clusters; c0 += 32 * J) {
+      float2 o[G][J];
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int t = rank + cs * (ew + EPI_NW * (i0 + g));
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          o[g][j] = t < tokens && c0 + 32 * j < clusters
+                        ? __ldcg(&p.stats[(size_t)t * clusters + c0 + 32 * j])
+                        : make_float2(-INFINITY, 0.0f);
+      }
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float mn = mg[g];
+#pragma unroll
+        for (int j = 0; j < J; ++j) mn = fmaxf(mn, o[g][j].x);
+        sg[g] = sg[g] == 0.0f ? 0.0f : sg[g] * exp2_approx((mg[g] - mn) * kLog2e);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          if (o[g][j].y != 0.0f) sg[g] += o[g][j].y * exp2_approx((o[g][j].x - mn) * kLog2e);
+        mg[g] = mn;
+      }
     }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const float top = warp_max(mg[g]);
+      const float sum =
+          warp_sum(sg[g] == 0.0f ? 0.0f : sg[g] * exp2_approx((mg[g] - top) * kLog2e));
+      if (lane == i0 + g) {
+        top_l = top;
+        sum_l = sum;
+      }
+    }
+  }
+  if (lane < 16 && t_l < tokens) {
+    const float ls = logf(sum_l);
+    p.loss[row_l] = (top_l - tsum_l) + ls;  // lse - target would lose lse's rounding
+    p.lse_out[row_l] = top_l + ls;
   }
 }
 
@@ -306,7 +332,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
         nlse_l = -p.lse[t_l] * kLog2e;
         rs_l = p.row_scale[t_l];
       }
-      if (EPI == S_STORE && p.row_of && p.slices == 1) row_l = p.row_of[t_l];
+      if ((EPI == S_STORE && p.row_of && p.slices == 1) || (EPI == S_STATS && t_l < tokens))
+        row_l = p.row_of[t_l];
     }
     float run_m = -INFINITY, run_s = 0.0f;  // S_STATS: lane i's token's
     bool done = true;
@@ -347,10 +374,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
       } else if (lane < cs) {
         mbar_arrive_remote(cluster_addr(&sm.ready, lane));
       }
-      if (!__all_sync(0xffffffffu, mbar_wait<true>(&sm.ready, lt & 1, sm, p.dev_err))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait_soon(&sm.ready, lt & 1, sm, p.dev_err))) break;
 
       // tokens rank + cs * (ew + 8 i) of this tile
       auto sum4 = [&](int t, int row) {  // 4 rows from `row` on
+        if (cs == 1) return *reinterpret_cast<const float4*>(sums + t * CM + row);
         const uint32_t at = (uint32_t)(t * CM + row) * 4u;
         float4 a = lds_cluster4(bases[0] + at);
 #pragma unroll
@@ -486,7 +514,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
     if constexpr (EPI == S_STATS) {
       // (after a wait that ran out, done is false in the whole warp and the error word set)
       if (done && rank + cs * ew < tokens)
-        stats_join(p, tokens, t0, tstep, rank, cs, ew, lane, run_m, run_s);
+        stats_join(p, tokens, t0, tstep, rank, cs, ew, lane, run_m, run_s, row_l, tsum_l);
     }
     __syncwarp();
     if (__any_sync(0xffffffffu, ovf) && lane == 0) set_dev_err(p.dev_err, MOE_DEVERR_RANGE);

@@ -124,6 +124,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, SM& sm
   return false;
 }
 
+// The same for a phase about to complete: polls for some microseconds first (a
+// thread woken from a suspended try_wait resumes later).  Cluster scope.
+template <class SM>
+__device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity, SM& sm,
+                                               int32_t* dev_err) {
+  for (int i = 0; i < 256; ++i)
+    if (mbar_test_wait(bar, parity)) return true;
+  return mbar_wait<true>(bar, parity, sm, dev_err);
+}
+
 // ---- pair form (clusters of two CTAs)
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
