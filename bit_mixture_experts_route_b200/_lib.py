@@ -753,10 +753,37 @@ def linear_ce_backward(dloss, X, W, targets, lse, ignore_index=-100, need_dx=Tru
     return dX, dW
 
 
+def _apart(grads, outs):
+    """What a call writes overlaps nothing else that it reads or writes: a tensor
+    listed twice would be scaled twice.  An ``out`` may be its gradient itself."""
+    spans = []
+    for i, g in enumerate(grads):
+        if g.numel() == 0:
+            continue
+        a, n = g.data_ptr(), g.numel() * g.element_size()
+        spans.append((a, a + n, f"grads[{i}]", outs is None))
+        if outs is not None and outs[i].data_ptr() != a:
+            spans.append((outs[i].data_ptr(), outs[i].data_ptr() + n, f"outs[{i}]", True))
+        elif outs is not None:
+            spans[-1] = (*spans[-1][:3], True)
+    spans.sort()
+    last = None  # of the spans so far, the one that reaches furthest
+    written = None  # and of the written ones
+    for s in spans:
+        for o in (last if s[3] else None, written):
+            if o is not None and s[0] < o[1]:
+                raise MoEError(f"grad_list: {o[2]} and {s[2]} overlap")
+        if last is None or s[1] > last[1]:
+            last = s
+        if s[3] and (written is None or s[1] > written[1]):
+            written = s
+
+
 class GradList:
     """The gradients of a model as ``grad_norm_clip`` takes them: the host
     arrays of addresses, sizes and types, built once and used every step.  It
-    holds the tensors, so the addresses stay valid."""
+    holds the tensors; one whose storage is replaced afterwards (``t.data =``,
+    ``t.set_``) needs a new list."""
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)
@@ -773,6 +800,7 @@ class GradList:
             _matrix(g, g.shape, f"grads[{i}]", g.dtype, self.device)
             if self.outs is not None:
                 _matrix(self.outs[i], g.shape, f"outs[{i}]", g.dtype, self.device)
+        _apart(self.grads, self.outs)
         self.n = n
         self._in = (ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads])
         self._numel = (ctypes.c_int64 * n)(*[g.numel() for g in self.grads])

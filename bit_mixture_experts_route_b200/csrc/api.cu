@@ -528,6 +528,17 @@ moe_status_t ce_shape(int T, int H, int V) {
   return MOE_OK;
 }
 
+// The body of an entry point: no C++ exception (the host-side caches may run out
+// of memory) leaves it.
+template <typename F>
+moe_status_t entry(F&& body) {
+  try {
+    return body();
+  } catch (...) {
+    return from_cuda(cudaErrorMemoryAllocation);
+  }
+}
+
 // A gradient over no rows: zeros.
 moe_status_t zero16(void* p, size_t n, void* stream) {
   if (!p) return MOE_OK;
@@ -566,8 +577,10 @@ moe_status_t moe_gated_ffn_forward(const void* X, moe_dtype_t dtype, const void*
   if (!workspace || workspace_bytes < moe_launch::gated_ffn_forward_workspace(T, H, I))
     return MOE_ERR_WORKSPACE;
   if (moe_status_t st = check_device()) return st;
-  return from_cuda(moe_launch::gated_ffn_forward(X, dtype, W_gu, W_d, T, H, I, residual, Y, gu,
+  return entry([&] {
+    return from_cuda(moe_launch::gated_ffn_forward(X, dtype, W_gu, W_d, T, H, I, residual, Y, gu,
                                                  workspace, dev_err, (cudaStream_t)stream));
+  });
 }
 
 moe_status_t moe_gated_ffn_backward(const void* dY, moe_dtype_t dtype, const void* X,
@@ -589,9 +602,11 @@ moe_status_t moe_gated_ffn_backward(const void* dY, moe_dtype_t dtype, const voi
     if (moe_status_t st = zero16(dW_gu, (size_t)2 * I * H, stream)) return st;
     return zero16(dW_d, (size_t)H * I, stream);
   }
-  return from_cuda(moe_launch::gated_ffn_backward(dY, dtype, X, gu, W_gu, W_d, T, H, I, dX, dW_gu,
+  return entry([&] {
+    return from_cuda(moe_launch::gated_ffn_backward(dY, dtype, X, gu, W_gu, W_d, T, H, I, dX, dW_gu,
                                                   dW_d, workspace, dev_err,
                                                   (cudaStream_t)stream));
+  });
 }
 
 moe_status_t moe_linear_ce_forward_workspace_size(int T, int H, int V, size_t* bytes) {
@@ -622,9 +637,11 @@ moe_status_t moe_linear_ce_forward(const void* X, moe_dtype_t dtype, const void*
   if (!workspace || workspace_bytes < moe_launch::linear_ce_workspace(T, H, V, false))
     return MOE_ERR_WORKSPACE;
   if (moe_status_t st = check_device()) return st;
-  return from_cuda(moe_launch::linear_ce_forward(X, dtype, W, targets, T, H, V, ignore_index,
+  return entry([&] {
+    return from_cuda(moe_launch::linear_ce_forward(X, dtype, W, targets, T, H, V, ignore_index,
                                                  loss, lse, workspace, dev_err,
                                                  (cudaStream_t)stream));
+  });
 }
 
 moe_status_t moe_linear_ce_backward(const float* dloss, const void* X, moe_dtype_t dtype,
@@ -643,9 +660,11 @@ moe_status_t moe_linear_ce_backward(const float* dloss, const void* X, moe_dtype
     return MOE_ERR_WORKSPACE;
   if (moe_status_t st = check_device()) return st;
   if (T == 0) return zero16(dW, (size_t)V * H, stream);
-  return from_cuda(moe_launch::linear_ce_backward(dloss, X, dtype, W, targets, lse, T, H, V,
+  return entry([&] {
+    return from_cuda(moe_launch::linear_ce_backward(dloss, X, dtype, W, targets, lse, T, H, V,
                                                   ignore_index, dX, dW, workspace, dev_err,
                                                   (cudaStream_t)stream));
+  });
 }
 
 moe_status_t moe_grad_norm_clip_workspace_size(int n, size_t* bytes) {
@@ -662,9 +681,11 @@ moe_status_t moe_grad_norm_clip(const void* const* grads, const int64_t* numel,
   if (n > 0 && (!grads || !numel || !dtypes)) return MOE_ERR_INVALID_ARG;
   if (!aligned16(workspace)) return MOE_ERR_MISALIGNED;
   if (reinterpret_cast<uintptr_t>(norm) & 3u) return MOE_ERR_MISALIGNED;
+  int64_t total = 0;
   for (int i = 0; i < n; ++i) {
-    if (!valid_dtype(dtypes[i]) || numel[i] < 0 || numel[i] > (INT64_C(1) << 42))
-      return MOE_ERR_INVALID_ARG;
+    if (!valid_dtype(dtypes[i]) || numel[i] < 0) return MOE_ERR_INVALID_ARG;
+    if (numel[i] > (INT64_C(1) << 42) - total) return MOE_ERR_UNSUPPORTED;
+    total += numel[i];
     if (numel[i] == 0) continue;
     const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]);
     const uintptr_t o = outs ? reinterpret_cast<uintptr_t>(outs[i]) : g;
@@ -675,8 +696,10 @@ moe_status_t moe_grad_norm_clip(const void* const* grads, const int64_t* numel,
   if (!workspace || workspace_bytes < moe_launch::grad_norm_clip_workspace(n))
     return MOE_ERR_WORKSPACE;
   if (moe_status_t st = check_device()) return st;
-  return from_cuda(moe_launch::grad_norm_clip(grads, numel, dtypes, n, max_norm, outs, norm,
+  return entry([&] {
+    return from_cuda(moe_launch::grad_norm_clip(grads, numel, dtypes, n, max_norm, outs, norm,
                                               workspace, dev_err, (cudaStream_t)stream));
+  });
 }
 
 }  // extern "C"

@@ -202,6 +202,17 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
+// The same as cuTensorMapEncodeTiled, through the looked-up entry.
+inline CUresult encode_tiled(CUtensorMap* out, CUtensorMapDataType dt, cuuint32_t rank, void* addr,
+                             const cuuint64_t* dims, const cuuint64_t* strides,
+                             const cuuint32_t* box, const cuuint32_t* estr,
+                             CUtensorMapInterleave il, CUtensorMapSwizzle sw,
+                             CUtensorMapL2promotion l2, CUtensorMapFloatOOBfill oob) {
+  const auto enc = tensor_map_encoder();
+  if (!enc) return CUDA_ERROR_NOT_SUPPORTED;
+  return enc(out, dt, rank, addr, dims, strides, box, estr, il, sw, l2, oob);
+}
+
 // A tensor map depends only on its arguments (address, sizes, strides, box,
 // swizzle, promotion, fill), so each distinct map is encoded once and reused:
 // a launch then costs a hash lookup instead of a driver call.  Same signature

@@ -584,16 +584,17 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
 #pragma unroll
           for (int i = 1; i < 32; ++i) cm = fmaxf(cm, __uint_as_float(v[i]));
           const float mn = fmaxf(m, cm);
-          const float mb = mn * kLog2e;
+          // differences first: a product with log2(e) rounds by 2^-24 of its own
+          // size, which for logits of hundreds is too much for the exponent
           float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
-            s0 += exp2_approx(fmaf(__uint_as_float(v[i]), kLog2e, -mb));
-            s1 += exp2_approx(fmaf(__uint_as_float(v[i + 1]), kLog2e, -mb));
-            s2 += exp2_approx(fmaf(__uint_as_float(v[i + 2]), kLog2e, -mb));
-            s3 += exp2_approx(fmaf(__uint_as_float(v[i + 3]), kLog2e, -mb));
+            s0 += exp2_approx((__uint_as_float(v[i]) - mn) * kLog2e);
+            s1 += exp2_approx((__uint_as_float(v[i + 1]) - mn) * kLog2e);
+            s2 += exp2_approx((__uint_as_float(v[i + 2]) - mn) * kLog2e);
+            s3 += exp2_approx((__uint_as_float(v[i + 3]) - mn) * kLog2e);
           }
-          s = s * exp2_approx(fmaf(m, kLog2e, -mb)) + ((s0 + s1) + (s2 + s3));
+          s = s * exp2_approx((m - mn) * kLog2e) + ((s0 + s1) + (s2 + s3));
           m = mn;
         }
         p.stats[(size_t)(HALVES * w.nt + hc) * p.rows_pad + row] = make_float2(m, s);
@@ -606,12 +607,15 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
             rows_end = second.M;
             dm = &second.d;
           }
-        float nlse = 0.f, rs = 0.f, tl = 0.f;
+        // p = exp(l - lse) by one FMA on l; what the product lse * log2(e) rounds
+        // off is common to the row and goes into its factor rp
+        float nlse = 0.f, rp = 0.f, pt = 0.f;
         int tgt = -1;
         if (EPI == E_DLOGITS) {
-          nlse = -p.lse[row] * kLog2e;
-          rs = p.row_scale[row];
-          tl = p.target_sum[row];
+          const float lse = p.lse[row], rs = p.row_scale[row];
+          nlse = -lse * kLog2e;
+          rp = rs * exp2_approx(-fmaf(lse, kLog2e, nlse));
+          pt = (exp2_approx((p.target_sum[row] - lse) * kLog2e) - 1.0f) * rs;
           tgt = p.targets[row] - p.col0 - w.nt * TN - hc * CW;
         }
 #pragma unroll 1
@@ -635,14 +639,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 v[i] = __float_as_uint(exp2_approx(fmaf(__uint_as_float(v[i]), kLog2e, nlse)));
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * rp);
               if ((unsigned)(tgt - c) < 32u) {
-                const float pt = exp2_approx(fmaf(tl, kLog2e, nlse)) - 1.0f;
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                   if (i == tgt - c) v[i] = __float_as_uint(pt);
               }
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * rs);
             } else {
               if (p.scale) {
 #pragma unroll
@@ -812,7 +815,7 @@ inline bool map_2d(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, in
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
   const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, es[2] = {1, 1};
-  return encode_tiled_cached(
+  return encode_tiled(
              m,
              std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
@@ -827,7 +830,7 @@ inline bool map_3d(CUtensorMap* m, const void* p, const int64_t (&d)[3], const i
   const cuuint64_t strides[2] = {(cuuint64_t)ld[0] * 2, (cuuint64_t)ld[1] * 2};
   const cuuint32_t box[3] = {(cuuint32_t)b[0], (cuuint32_t)b[1], (cuuint32_t)b[2]},
                    es[3] = {1, 1, 1};
-  return encode_tiled_cached(
+  return encode_tiled(
              m,
              std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,

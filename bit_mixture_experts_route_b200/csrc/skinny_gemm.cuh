@@ -322,14 +322,14 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
     // the epilogue needs to know of the i-th
     const int t_l = rank + cs * (ew + EPI_NW * lane);
     int tgt_l = -1, row_l = t_l;
-    float tsum_l = 0.0f, nlse_l = 0.0f, rs_l = 0.0f;
+    float tsum_l = 0.0f, lse_l = 0.0f, rs_l = 0.0f;
     if (lane < 16 && t_l < joined) {
       if (EPI == S_STATS || EPI == S_DLOGITS) {
         tgt_l = p.targets[t_l];
         tsum_l = p.target_sum[t_l];
       }
       if (EPI == S_DLOGITS) {
-        nlse_l = -p.lse[t_l] * kLog2e;
+        lse_l = p.lse[t_l];
         rs_l = p.row_scale[t_l];
       }
       if ((EPI == S_STORE && p.row_of && p.slices == 1) || (EPI == S_STATS && t_l < tokens))
@@ -486,14 +486,14 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
               run_m = mn;
             }
           } else {  // S_DLOGITS
-            const float nlse = __shfl_sync(0xffffffffu, nlse_l, i);
+            const float lse = __shfl_sync(0xffffffffu, lse_l, i);
             const float rs = __shfl_sync(0xffffffffu, rs_l, i);
             const float tsum = __shfl_sync(0xffffffffu, tsum_l, i);
             const int tgt = __shfl_sync(0xffffffffu, tgt_l, i) - col;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float x = exp2_approx(fmaf(v[e], kLog2e, nlse));
-              if (tgt == e) x = exp2_approx(fmaf(tsum, kLog2e, nlse)) - 1.0f;
+              float x = exp2_approx((v[e] - lse) * kLog2e);
+              if (tgt == e) x = exp2_approx((tsum - lse) * kLog2e) - 1.0f;
               v[e] = x * rs;
             }
             // rows of out are p.ld >= 128 tiles long: the last tile's end is theirs too
