@@ -580,6 +580,12 @@ def _matrix(t, shape, name, dtype, device):
         raise MoEError(f"{name} is on {t.device}, the call's tensors are on {device}")
 
 
+def _given(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise MoEError(f"{name} must be a CUDA tensor")
+
+
 def _raw_stream(device):
     """The address of ``device``'s current stream; the cheap way where there is one."""
     if device.index is not None and _current_raw_stream is not None:
@@ -625,11 +631,21 @@ def gated_ffn_backward_workspace_size(T, H, I):
 
 
 def _ffn_shapes(X, W_gu, W_d):
+    dt = getattr(X, "dtype", None)
+    if dt is torch.bfloat16 or dt is torch.float16:
+        # the well-formed call, by as few looks as it takes; what fails is named below
+        dev, xs, ws = X.device, X.shape, getattr(W_d, "shape", ())
+        if (len(xs) == 2 and len(ws) == 2 and ws[0] == xs[1] and X.is_cuda and W_d.dtype is dt
+                and isinstance(W_gu, torch.Tensor) and W_gu.dtype is dt
+                and W_gu.shape == (2 * ws[1], xs[1]) and W_d.device == dev and W_gu.device == dev
+                and X.is_contiguous() and W_d.is_contiguous() and W_gu.is_contiguous()):
+            return xs[0], xs[1], ws[1]
     if not isinstance(X, torch.Tensor) or X.dtype not in _HALF:
         raise MoEError("X must be a bf16 or fp16 tensor")
     _need(X, X.dtype, "X", 2)
-    if not isinstance(W_d, torch.Tensor) or W_d.dim() != 2:
-        raise MoEError("W_d must be a tensor of 2 dims")
+    for name, t in (("W_gu", W_gu), ("W_d", W_d)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise MoEError(f"{name} must be a tensor of 2 dims")
     dt, dev = X.dtype, X.device
     T, H = X.shape
     I = W_d.shape[1]
@@ -661,8 +677,8 @@ def gated_ffn_forward(X, W_gu, W_d, residual=None, save_gu=False, workspace=None
         if gu is None and save_gu:
             gu = X.new_empty((T, 2 * I))
         _check(load().moe_gated_ffn_forward(
-            _at(X), DT[X.dtype], _at(W_gu), _at(W_d), T, H, I, _at(residual), _at(out),
-            _at(gu), _at(ws), ws.numel(), _at(dev_err), _raw_stream(dev)), "moe_gated_ffn_forward")
+            X.data_ptr(), DT[X.dtype], W_gu.data_ptr(), W_d.data_ptr(), T, H, I, _at(residual), out.data_ptr(),
+            _at(gu), ws.data_ptr(), ws.numel(), _at(dev_err), _raw_stream(dev)), "moe_gated_ffn_forward")
     return out if gu is None else (out, gu)
 
 
@@ -673,6 +689,7 @@ def gated_ffn_backward(dY, X, gu, W_gu, W_d, need_dx=True, need_dw=True, workspa
     what ``need_dx`` / ``need_dw`` leave out."""
     T, H, I = _ffn_shapes(X, W_gu, W_d)
     dev = X.device
+    _given(dY=dY, gu=gu)
     _matrix(dY, (T, H), "dY", X.dtype, dev)
     _matrix(gu, (T, 2 * I), "gu", X.dtype, dev)
     _dev_word(dev_err, dev)
@@ -684,8 +701,8 @@ def gated_ffn_backward(dY, X, gu, W_gu, W_d, need_dx=True, need_dw=True, workspa
         dW_gu = torch.empty_like(W_gu) if need_dw else None
         dW_d = torch.empty_like(W_d) if need_dw else None
         _check(load().moe_gated_ffn_backward(
-            _at(dY), DT[X.dtype], _at(X), _at(gu), _at(W_gu), _at(W_d), T, H, I, _at(dX),
-            _at(dW_gu), _at(dW_d), _at(ws), ws.numel(), _at(dev_err), _raw_stream(dev)),
+            dY.data_ptr(), DT[X.dtype], X.data_ptr(), gu.data_ptr(), W_gu.data_ptr(), W_d.data_ptr(), T, H, I, _at(dX),
+            _at(dW_gu), _at(dW_d), ws.data_ptr(), ws.numel(), _at(dev_err), _raw_stream(dev)),
             "moe_gated_ffn_backward")
     return dX, dW_gu, dW_d
 
@@ -706,6 +723,7 @@ def _ce_shapes(X, W, targets):
         raise MoEError("W must be a tensor of 2 dims")
     T, H = X.shape
     V = W.shape[0]
+    _given(targets=targets)
     _matrix(W, (V, H), "W", X.dtype, X.device)
     _matrix(targets, (T,), "targets", torch.int32, X.device)
     return T, H, V
@@ -724,8 +742,8 @@ def linear_ce_forward(X, W, targets, ignore_index=-100, workspace=None, dev_err=
         loss = torch.empty(T, dtype=torch.float32, device=dev)
         lse = torch.empty_like(loss)
         _check(load().moe_linear_ce_forward(
-            _at(X), DT[X.dtype], _at(W), _at(targets), T, H, V, ignore_index, _at(loss),
-            _at(lse), _at(ws), ws.numel(), _at(dev_err), _raw_stream(dev)),
+            X.data_ptr(), DT[X.dtype], W.data_ptr(), targets.data_ptr(), T, H, V, ignore_index, loss.data_ptr(),
+            lse.data_ptr(), ws.data_ptr(), ws.numel(), _at(dev_err), _raw_stream(dev)),
             "moe_linear_ce_forward")
     return loss, lse
 
@@ -737,6 +755,7 @@ def linear_ce_backward(dloss, X, W, targets, lse, ignore_index=-100, need_dx=Tru
     type; ``None`` for what ``need_dx`` / ``need_dw`` leave out."""
     T, H, V = _ce_shapes(X, W, targets)
     dev = X.device
+    _given(dloss=dloss, lse=lse)
     _matrix(dloss, (T,), "dloss", torch.float32, dev)
     _matrix(lse, (T,), "lse", torch.float32, dev)
     _dev_word(dev_err, dev)
@@ -747,8 +766,8 @@ def linear_ce_backward(dloss, X, W, targets, lse, ignore_index=-100, need_dx=Tru
         dX = torch.empty_like(X) if need_dx else None
         dW = torch.empty_like(W) if need_dw else None
         _check(load().moe_linear_ce_backward(
-            _at(dloss), _at(X), DT[X.dtype], _at(W), _at(targets), _at(lse), T, H, V,
-            ignore_index, _at(dX), _at(dW), _at(ws), ws.numel(), _at(dev_err), _raw_stream(dev)),
+            dloss.data_ptr(), X.data_ptr(), DT[X.dtype], W.data_ptr(), targets.data_ptr(), lse.data_ptr(), T, H, V,
+            ignore_index, _at(dX), _at(dW), ws.data_ptr(), ws.numel(), _at(dev_err), _raw_stream(dev)),
             "moe_linear_ce_backward")
     return dX, dW
 
@@ -832,6 +851,6 @@ def grad_norm_clip(grads, max_norm, norm=None, workspace=None, dev_err=None):
         if norm is None:
             norm = torch.empty(1, dtype=torch.float32, device=dev)
         _check(load().moe_grad_norm_clip(
-            grads._in, grads._numel, grads._dt, grads.n, max_norm, grads._out, _at(norm),
-            _at(ws), ws.numel(), _at(dev_err), _raw_stream(dev)), "moe_grad_norm_clip")
+            grads._in, grads._numel, grads._dt, grads.n, max_norm, grads._out, norm.data_ptr(),
+            ws.data_ptr(), ws.numel(), _at(dev_err), _raw_stream(dev)), "moe_grad_norm_clip")
     return norm

@@ -1068,8 +1068,10 @@ __global__ void __launch_bounds__(256 * finish_groups<FIN>()) finish_kernel(Fini
       for (int e = 0; e < 8; ++e) v[e] *= sc;
     }
     if (p.residual) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += p.residual[at + e];
+      const float4 a = *reinterpret_cast<const float4*>(p.residual + at);
+      const float4 b = *reinterpret_cast<const float4*>(p.residual + at + 4);
+      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
     }
     put(p.out, at, v);
   } else if (FIN == F_SWIGLU) {

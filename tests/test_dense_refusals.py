@@ -170,6 +170,11 @@ def test_binding_ffn(lib):
            lambda: _lib.gated_ffn_forward(X, Wgu, Wd, workspace=torch.zeros(9, dtype=torch.uint8)),
            lambda: _lib.gated_ffn_forward(X, Wgu, Wd, dev_err=torch.zeros(1)),
            lambda: _lib.gated_ffn_forward(None, Wgu, Wd),
+           lambda: _lib.gated_ffn_forward(X, None, Wd),
+           lambda: _lib.gated_ffn_forward(X, Wgu, None),
+           lambda: _lib.gated_ffn_forward(X, Wgu, Wd[0]),
+           lambda: _lib.gated_ffn_backward(None, X, gu, Wgu, Wd),
+           lambda: _lib.gated_ffn_backward(dY, X, None, Wgu, Wd),
            lambda: _lib.gated_ffn_backward(dY[:3], X, gu, Wgu, Wd),
            lambda: _lib.gated_ffn_backward(dY, X, gu[:, :48], Wgu, Wd),
            lambda: _lib.gated_ffn_backward(dY, X, gu, Wgu, Wd, need_dx=False, need_dw=False)]
@@ -191,6 +196,10 @@ def test_binding_linear_ce(lib):
            lambda: _lib.linear_ce_forward(X, W.half(), y),
            lambda: _lib.linear_ce_forward(X, b16(101, 72), y),
            lambda: _lib.linear_ce_forward(X, b16(202, 64)[::2], y),
+           lambda: _lib.linear_ce_forward(X, W, None),
+           lambda: _lib.linear_ce_forward(X, None, y),
+           lambda: _lib.linear_ce_backward(None, X, W, y, f32),
+           lambda: _lib.linear_ce_backward(f32, X, W, y, None),
            lambda: _lib.linear_ce_backward(f32[:2], X, W, y, f32),
            lambda: _lib.linear_ce_backward(f32, X, W, y, f32.double()),
            lambda: _lib.linear_ce_backward(f32, X, W, y, f32, need_dx=False, need_dw=False)]
