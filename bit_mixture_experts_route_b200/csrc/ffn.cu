@@ -91,10 +91,8 @@ cudaError_t forward(const void* X, const void* W_gu, const void* W_d, int M, int
                     const float* residual, void* Y, void* gu, void* ws, int32_t* dev_err,
                     cudaStream_t s) {
   void* h = ws;
-  if (M <= 8)
-    return launch_ffn_gemv<T, 1>(X, W_gu, W_d, M, H, I, residual, Y, gu, h, dev_err, s);
-  if (M <= kGemvRows)
-    return launch_ffn_gemv<T, 2>(X, W_gu, W_d, M, H, I, residual, Y, gu, h, dev_err, s);
+  if (use_gemv(M, H, I))
+    return launch_ffn_gemv<T>(X, W_gu, W_d, M, H, I, residual, Y, gu, h, dev_err, s);
   if (M <= kSkinnyRows) {
     SkinnyArgs a = {};
     a.M = M;
@@ -271,7 +269,7 @@ using namespace moe;
 
 size_t gated_ffn_forward_workspace(int M, int H, int I) {
   const size_t h = align1k((size_t)M * I * 2);
-  if (M <= kGemvRows) return h;
+  if (use_gemv(M, H, I)) return h;
   if (M <= kSkinnyRows) return h + skinny_part_bytes(M, H, I);
   return h + std::max(part_bytes(M, 2 * (int64_t)I, H), part_bytes(M, H, I));
 }

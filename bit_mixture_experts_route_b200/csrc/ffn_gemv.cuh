@@ -5,7 +5,7 @@
 //
 // A block owns 16 weight rows (up: 8 gate rows and their 8 up rows, which land
 // in the same thread's accumulators; down: 16 output rows) and its eight warps
-// take every eighth 32-k chunk of them.  The sum over k does not depend on
+// take every eighth 64-k chunk of them.  The sum over k does not depend on
 // which k sits in which MMA slot, so a thread feeds the 16 consecutive bytes
 // that it loads (8 k of its row) to two MMAs as they are and loads the tokens'
 // rows in the same pattern: wide loads, no shuffles, no shared memory but for
@@ -21,8 +21,24 @@ namespace moe {
 namespace dense {
 
 constexpr int kGemvWarps = 8;
-constexpr int kGemvUnroll = 8;  // 32-k chunks in flight per warp: 16 x 16 bytes a thread
+constexpr int kGemvK = 64;      // k of a chunk: a 128-byte line of each of its rows
+// Half chunks in flight per warp (UNROLL).  Fewer let more blocks share an SM,
+// which streams better; more take a short row in one round of loads.  8 tokens,
+// 4 against 2: 2048 x 1024 (13 MB) 7.4 and 8.5 us, 2048 x 4096 (50 MB) 17.3 and
+// 14.8 us, 4096 x 4096 (101 MB) 28.6 and 24.4 us.  Two groups of 8 tokens read
+// the tokens twice as often; 16 tokens, 4 against 8: 256 x 8192 (13 MB) 11.5 and
+// 14.0 us, 2048 x 4096 24 and 19 us.
+inline bool gemv_streams(int H, int I) { return (int64_t)6 * H * I > 32 << 20; }
 constexpr int kGemvRows = 16;   // tokens at most
+
+// Whether so many tokens take these kernels.  Beyond some size of the weights the
+// tensor-core form streams them as fast or faster: 4096 x 8192 (201 MB) in 43 us
+// against 53 us for 8 tokens and 65 us for 16; 4096 x 4096 (101 MB) in 28 against
+// 24 and 35 us; 2048 x 4096 (50 MB) in 21 against 15 and 19 us.
+inline bool use_gemv(int M, int H, int I) {
+  const int64_t bytes = (int64_t)6 * H * I;
+  return M <= 8 ? bytes <= 128 << 20 : M <= kGemvRows && bytes <= 64 << 20;
+}
 
 template <typename T>
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -52,7 +68,7 @@ __device__ __forceinline__ float2 lds_cluster2(uint32_t a) {
 // tokens.  K and rows are multiples of 8.  The down form is launched right
 // behind the up form, so its weights cannot be anyone's pending output: it
 // loads the first of them before it waits for h.
-template <typename T, int NT, bool UP>
+template <typename T, int NT, bool UP, int UNROLL>
 __global__ void __launch_bounds__(32 * kGemvWarps) ffn_gemv_kernel(
     const T* __restrict__ A, const T* __restrict__ X, int M, int rows, int K,
     const float* __restrict__ residual, T* __restrict__ out, T* __restrict__ gu,
@@ -80,16 +96,16 @@ __global__ void __launch_bounds__(32 * kGemvWarps) ffn_gemv_kernel(
     xp[n] = X + (size_t)(live[n] ? 8 * n + g : 0) * K + 8 * t;
   }
   float acc[NT][4] = {};
-  const int chunks = (K + 31) / 32;
+  const int chunks = (K + kGemvK - 1) / kGemvK;
   const int lo = chunks * rank / cs, hi = chunks * (rank + 1) / cs;  // this block's
-  const int kend = min(K, 32 * hi);
+  const int kend = min(K, kGemvK * hi);
   const uint4 zero = make_uint4(0, 0, 0, 0);
   bool first = !UP;
-  for (int c0 = lo + warp; c0 < hi; c0 += kGemvWarps * kGemvUnroll) {
-    uint4 a0[kGemvUnroll], a1[kGemvUnroll];
+  for (int c0 = lo + warp; c0 < hi; c0 += kGemvWarps * UNROLL / 2) {
+    uint4 a0[UNROLL], a1[UNROLL];
 #pragma unroll
-    for (int i = 0; i < kGemvUnroll; ++i) {
-      const int k = 32 * (c0 + i * kGemvWarps);
+    for (int i = 0; i < UNROLL; ++i) {
+      const int k = kGemvK * (c0 + (i >> 1) * kGemvWarps) + 32 * (i & 1);
       const bool in = k + 8 * t < kend;
       a0[i] = in ? ldg_stream_u4(a0p + k) : zero;
       a1[i] = in ? ldg_stream_u4(a1p + k) : zero;
@@ -100,8 +116,8 @@ __global__ void __launch_bounds__(32 * kGemvWarps) ffn_gemv_kernel(
       first = false;
     }
 #pragma unroll
-    for (int i = 0; i < kGemvUnroll; ++i) {
-      const int k = 32 * (c0 + i * kGemvWarps);
+    for (int i = 0; i < UNROLL; ++i) {
+      const int k = kGemvK * (c0 + (i >> 1) * kGemvWarps) + 32 * (i & 1);
       if (k >= kend) break;
       const bool in = k + 8 * t < kend;
 #pragma unroll
@@ -184,21 +200,21 @@ __global__ void __launch_bounds__(32 * kGemvWarps) ffn_gemv_kernel(
   if (ovf) set_dev_err(dev_err, MOE_DEVERR_RANGE);
 }
 
-// Blocks per row block: until one round of loads (8 warps x 8 chunks of 32 k) or
-// four blocks per SM is reached.  464 x 7712, 5 tokens: one block a row block
-// took 15 us.
-inline int gemv_cluster(int blocks, int K) {
+// Blocks per row block: until one round of loads or four blocks per SM is reached.  464 x 7712, 5
+// tokens: one block a row block took 15 us.
+inline int gemv_cluster(int blocks, int K, int unroll) {
   int c = 1;
-  while (c < 8 && K > c * 32 * kGemvWarps * kGemvUnroll && 2 * c * blocks <= 4 * device_sm_count())
+  while (c < 8 && K > c * 32 * kGemvWarps * unroll && 2 * c * blocks <= 4 * device_sm_count())
     c *= 2;
   return c;
 }
 
-template <typename T, int NT, bool UP>
+template <typename T, int NT, bool UP, int UNROLL>
 cudaError_t launch_gemv(const void* A, const void* X, int M, int rows, int K,
                         const float* residual, void* out, void* gu, int32_t* dev_err,
                         cudaStream_t s) {
-  const int blocks = UP ? rows / 8 : ceil_div(rows, 16), c = gemv_cluster(blocks, K);
+  const int blocks = UP ? rows / 8 : ceil_div(rows, 16),
+            c = gemv_cluster(blocks, K, UNROLL);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks * c);
   cfg.blockDim = dim3(32 * kGemvWarps);
@@ -212,18 +228,32 @@ cudaError_t launch_gemv(const void* A, const void* X, int M, int rows, int K,
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = c > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, ffn_gemv_kernel<T, NT, UP>, static_cast<const T*>(A),
+  return cudaLaunchKernelEx(&cfg, ffn_gemv_kernel<T, NT, UP, UNROLL>, static_cast<const T*>(A),
                             static_cast<const T*>(X), M, rows, K, residual, static_cast<T*>(out),
                             static_cast<T*>(gu), dev_err);
 }
 
-template <typename T, int NT>
+template <typename T, int NT, int UNROLL>
+cudaError_t launch_both(const void* X, const void* W_gu, const void* W_d, int M, int H, int I,
+                        const float* residual, void* Y, void* gu, void* h, int32_t* dev_err,
+                        cudaStream_t s) {
+  if (cudaError_t e =
+          launch_gemv<T, NT, true, UNROLL>(W_gu, X, M, I, H, nullptr, h, gu, dev_err, s))
+    return e;
+  return launch_gemv<T, NT, false, UNROLL>(W_d, h, M, H, I, residual, Y, nullptr, dev_err, s);
+}
+
+template <typename T>
 cudaError_t launch_ffn_gemv(const void* X, const void* W_gu, const void* W_d, int M, int H, int I,
                             const float* residual, void* Y, void* gu, void* h, int32_t* dev_err,
                             cudaStream_t s) {
-  if (cudaError_t e = launch_gemv<T, NT, true>(W_gu, X, M, I, H, nullptr, h, gu, dev_err, s))
-    return e;
-  return launch_gemv<T, NT, false>(W_d, h, M, H, I, residual, Y, nullptr, dev_err, s);
+  const bool streams = gemv_streams(H, I);
+  if (M > 8)
+    return streams
+               ? launch_both<T, 2, 8>(X, W_gu, W_d, M, H, I, residual, Y, gu, h, dev_err, s)
+               : launch_both<T, 2, 4>(X, W_gu, W_d, M, H, I, residual, Y, gu, h, dev_err, s);
+  return streams ? launch_both<T, 1, 2>(X, W_gu, W_d, M, H, I, residual, Y, gu, h, dev_err, s)
+                 : launch_both<T, 1, 4>(X, W_gu, W_d, M, H, I, residual, Y, gu, h, dev_err, s);
 }
 
 }  // namespace dense

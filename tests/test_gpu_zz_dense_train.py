@@ -65,7 +65,7 @@ def ffn_ref(X, Wgu, Wd, residual=None):
 
 
 # rows from one to several tiles, widths that fill no tile, splits along k and none
-FFN = [(33, 256, 8192), (5, 464, 7712), (12, 4096, 256), (9, 264, 4200), (400, 640, 1504), (1, 256, 256), (64, 8, 8), (90, 264, 1000), (96, 2048, 512), (128, 512, 1096), (129, 264, 72), (1, 2048, 1024), (3, 8, 8), (17, 72, 520), (32, 1024, 2048), (40, 136, 264),
+FFN = [(3, 2056, 4096), (11, 2048, 4096), (2, 4096, 8192), (14, 4096, 4096), (33, 256, 8192), (5, 464, 7712), (12, 4096, 256), (9, 264, 4200), (400, 640, 1504), (1, 256, 256), (64, 8, 8), (90, 264, 1000), (96, 2048, 512), (128, 512, 1096), (129, 264, 72), (1, 2048, 1024), (3, 8, 8), (17, 72, 520), (32, 1024, 2048), (40, 136, 264),
        (255, 256, 128), (256, 512, 384), (257, 264, 1032), (300, 1000, 2744), (1024, 512, 256),
        (2049, 384, 640)]
 
