@@ -576,9 +576,8 @@ moe_status_t moe_layer_forward(const void* X, const float* logits, int T,
  *   gu        [T, 2I] or NULL: g | u, rounded once, for the backward call
  *   dev_err   int32 device word or NULL; MOE_DEVERR_RANGE when an F16 h, g, u
  *             or Y overflowed, MOE_DEVERR_TIMEOUT
- * Both projections, the activation and the product are one launch (tcgen05);
- * sums are fp32, h is rounded once to dtype (it is the second product's
- * operand).  Pointers 16-byte aligned; Y and gu must not overlap the inputs.
+ * Both projections, the activation and the product are one launch; sums are
+ * fp32, h is rounded once to dtype (it is the second product's operand).  Pointers 16-byte aligned; Y and gu must not overlap the inputs.
  * T == 0 enqueues nothing.
  */
 moe_status_t moe_gated_ffn_forward_workspace_size(int T, int H, int I, size_t* bytes);
@@ -657,6 +656,7 @@ moe_status_t moe_linear_ce_backward(const float* dloss, const void* X, moe_dtype
  *   outs      NULL or outs[i] == grads[i]: in place (nothing is written when
  *             the factor is 1); otherwise a tensor of the same size and type.
  *             Tensors must not overlap one another
+ *             Together at most 2^42 elements (beyond: MOE_ERR_UNSUPPORTED)
  *   max_norm  >= 0; INFINITY gives the norm alone
  *   norm      fp32 [1] (device); a finite norm beyond fp32's range reads as
  *             infinity, the clipping still uses its fp64 value
