@@ -715,7 +715,9 @@ def linear_ce_backward_workspace_size(T, H, V):
     return _size("moe_linear_ce_backward_workspace_size", T, H, V)
 
 
-def _ce_shapes(X, W, targets):
+def _ce_shapes(X, W, targets, ignore_index):
+    if not -2 ** 31 <= ignore_index < 2 ** 31:
+        raise MoEError(f"ignore_index {ignore_index} is no int32")
     if not isinstance(X, torch.Tensor) or X.dtype not in _HALF:
         raise MoEError("X must be a bf16 or fp16 tensor")
     _need(X, X.dtype, "X", 2)
@@ -734,7 +736,7 @@ def linear_ce_forward(X, W, targets, ignore_index=-100, workspace=None, dev_err=
     H]``, ``W [V, H]`` (both bf16 or both fp16), ``targets`` int32 ``[T]`` ->
     ``(loss fp32 [T], lse fp32 [T])``, both 0 in rows whose target is
     ``ignore_index``."""
-    T, H, V = _ce_shapes(X, W, targets)
+    T, H, V = _ce_shapes(X, W, targets, ignore_index)
     dev = X.device
     _dev_word(dev_err, dev)
     with _on(dev):
@@ -753,7 +755,7 @@ def linear_ce_backward(dloss, X, W, targets, lse, ignore_index=-100, need_dx=Tru
     """Gradients of ``linear_ce_forward`` for the upstream ``dloss`` fp32
     ``[T]`` and the forward's ``lse``: ``(dX [T, H], dW [V, H])`` of the inputs'
     type; ``None`` for what ``need_dx`` / ``need_dw`` leave out."""
-    T, H, V = _ce_shapes(X, W, targets)
+    T, H, V = _ce_shapes(X, W, targets, ignore_index)
     dev = X.device
     _given(dloss=dloss, lse=lse)
     _matrix(dloss, (T,), "dloss", torch.float32, dev)

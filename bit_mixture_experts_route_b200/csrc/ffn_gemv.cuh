@@ -57,6 +57,15 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// A plain (coherent) load: X is the launch before's output, written while this
+// kernel may already have started, which a read-only load would not allow for.
+__device__ __forceinline__ uint4 ldg_u4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
 __device__ __forceinline__ float2 lds_cluster2(uint32_t a) {
   float2 v;
   asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
@@ -70,7 +79,7 @@ __device__ __forceinline__ float2 lds_cluster2(uint32_t a) {
 // loads the first of them before it waits for h.
 template <typename T, int NT, bool UP, int UNROLL>
 __global__ void __launch_bounds__(32 * kGemvWarps) ffn_gemv_kernel(
-    const T* __restrict__ A, const T* __restrict__ X, int M, int rows, int K,
+    const T* __restrict__ A, const T* X, int M, int rows, int K,
     const float* __restrict__ residual, T* __restrict__ out, T* __restrict__ gu,
     int32_t* dev_err) {
   __shared__ float sums[kGemvWarps][NT][32][4];
@@ -122,7 +131,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps) ffn_gemv_kernel(
       const bool in = k + 8 * t < kend;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const uint4 b = in && live[n] ? *reinterpret_cast<const uint4*>(xp[n] + k) : zero;
+        const uint4 b = in && live[n] ? ldg_u4(xp[n] + k) : zero;
         mma_16x8x16<T>(acc[n], a0[i].x, a1[i].x, a0[i].y, a1[i].y, b.x, b.y);
         mma_16x8x16<T>(acc[n], a0[i].z, a1[i].z, a0[i].w, a1[i].w, b.z, b.w);
       }

@@ -231,7 +231,7 @@ __device__ __forceinline__ float factor_of(double sum, float max_norm, float* no
 
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, 6) squares_kernel(const __grid_constant__ Table<CAP> t,
-                                                              double* __restrict__ part) {
+                                                              double* part) {
   pdl_wait();
   pdl_trigger();
   double sum = 0.0;
@@ -241,9 +241,11 @@ __global__ void __launch_bounds__(kThreads, 6) squares_kernel(const __grid_const
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
+// (part is no restricted pointer: the launch before may still write it when this
+// one starts, so it must not be read by read-only loads)
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, 4)
-    scale_kernel(const __grid_constant__ Table<CAP> t, const double* __restrict__ part, int parts,
+    scale_kernel(const __grid_constant__ Table<CAP> t, const double* part, int parts,
                  float max_norm, float* __restrict__ norm_out, int first, int32_t* dev_err) {
   pdl_wait();
   pdl_trigger();

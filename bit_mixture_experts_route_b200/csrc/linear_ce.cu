@@ -272,10 +272,10 @@ __global__ void __launch_bounds__(256) ce_gather_kernel(const GatherArgs p, int 
 // The (max, sum) pieces of 32 rows: warp w joins pieces w, w + W, ..., then the
 // first warp joins the warps in order.
 constexpr int kJoinWarps = 32;
+// (no restricted pointers: the launch before may still write when this one starts)
 __global__ void __launch_bounds__(32 * kJoinWarps) ce_join_kernel(
-    const float2* __restrict__ stats, int pieces, int rows_pad, const float* __restrict__ tsum,
-    const Meta* __restrict__ meta, const int* __restrict__ row_of, float* __restrict__ loss,
-    float* __restrict__ lse) {
+    const float2* stats, int pieces, int rows_pad, const float* tsum, const Meta* meta,
+    const int* row_of, float* loss, float* lse) {
   __shared__ float2 part[kJoinWarps][32];
   pdl_wait();
   pdl_trigger();

@@ -577,7 +577,8 @@ moe_status_t moe_layer_forward(const void* X, const float* logits, int T,
  *   dev_err   int32 device word or NULL; MOE_DEVERR_RANGE when an F16 h, g, u
  *             or Y overflowed, MOE_DEVERR_TIMEOUT
  * Both projections, the activation and the product are one launch; sums are
- * fp32, h is rounded once to dtype (it is the second product's operand).  Pointers 16-byte aligned; Y and gu must not overlap the inputs.
+ * fp32, h is rounded once to dtype (it is the second product's operand).
+ * Pointers 16-byte aligned; Y and gu must not overlap the inputs.
  * T == 0 enqueues nothing.
  */
 moe_status_t moe_gated_ffn_forward_workspace_size(int T, int H, int I, size_t* bytes);

@@ -197,6 +197,8 @@ def test_binding_linear_ce(lib):
            lambda: _lib.linear_ce_forward(X, b16(101, 72), y),
            lambda: _lib.linear_ce_forward(X, b16(202, 64)[::2], y),
            lambda: _lib.linear_ce_forward(X, W, None),
+           lambda: _lib.linear_ce_forward(X, W, y, ignore_index=1 << 40),
+           lambda: _lib.linear_ce_backward(f32, X, W, y, f32, ignore_index=-(1 << 31) - 1),
            lambda: _lib.linear_ce_forward(X, None, y),
            lambda: _lib.linear_ce_backward(None, X, W, y, f32),
            lambda: _lib.linear_ce_backward(f32, X, W, y, None),

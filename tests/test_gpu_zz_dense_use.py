@@ -303,6 +303,39 @@ def test_ffn_range_and_infinities(T):
     assert (dWd[:, :36] == 0).all() and (dWgu[:36] == 0).all() and (dWgu[72:108] == 0).all()
 
 
+@pytest.mark.parametrize("T", [20, 300])
+def test_ffn_each_gradient_alone(T):
+    # the C call takes any subset; the binding asks for both weights or none
+    H, I = 72, 136
+    c = ffn_case(T, H, I)
+    _, gu = moe.gated_ffn_forward(c["X"], c["W_gu"], c["W_d"], save_gu=True)
+    want = moe.gated_ffn_backward(c["dY"], c["X"], gu, c["W_gu"], c["W_d"])
+    ws = torch.empty(moe.gated_ffn_backward_workspace_size(T, H, I), dtype=torch.uint8,
+                     device="cuda")
+    for i in range(3):
+        out = [torch.empty_like(w) if i == j else None for j, w in enumerate(want)]
+        st = moe.load().moe_gated_ffn_backward(
+            c["dY"].data_ptr(), 1, c["X"].data_ptr(), gu.data_ptr(), c["W_gu"].data_ptr(),
+            c["W_d"].data_ptr(), T, H, I, *[None if o is None else o.data_ptr() for o in out],
+            ws.data_ptr(), ws.numel(), None, torch.cuda.current_stream().cuda_stream)
+        assert st == 0
+        # alone, a product may be split along k in another way
+        close = (out[i].double() - want[i].double()).abs()
+        size = want[i].double().abs() + want[i].double().abs().mean()
+        assert (close <= 2 * U[torch.bfloat16] * size).all()
+
+
+def test_clip_of_nothing_and_limits():
+    empty = torch.empty(0, device="cuda")
+    assert float(moe.grad_norm_clip([empty, empty[:0]], 1.0)) == 0.0
+    for n in (100, 2_000_000):
+        t = torch.ones(n, device="cuda")
+        assert float(moe.grad_norm_clip([t], math.inf)) == pytest.approx(math.sqrt(n), rel=1e-6)
+        assert (t == 1).all()
+        moe.grad_norm_clip([t], 0.0)
+        assert (t == 0).all()
+
+
 def test_clip_uses_what_the_list_holds_each_step():
     g = gen(2)
     grads = [randn(g, 4000), randn(g, 70001, dtype=torch.bfloat16)]
