@@ -100,8 +100,7 @@ __device__ __forceinline__ float4 lds_cluster4(uint32_t a) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(a)
-               : "memory");
+               : "r"(a));
   return v;
 }
 
@@ -380,13 +379,15 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
       auto sum4 = [&](int t, int row) {  // 4 rows from `row` on
         if (cs == 1) return *reinterpret_cast<const float4*>(sums + t * CM + row);
         const uint32_t at = (uint32_t)(t * CM + row) * 4u;
-        float4 a = lds_cluster4(bases[0] + at);
+        float4 b[8];  // all ranks' loads in flight, then the sum in rank order
 #pragma unroll
-        for (int r = 1; r < 8; ++r)
-          if (r < cs) {
-            const float4 b = lds_cluster4(bases[r] + at);
-            a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
-          }
+        for (int r = 0; r < 8; ++r)
+          b[r] = r < cs ? lds_cluster4(bases[r] + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 a = b[0];
+#pragma unroll
+        for (int r = 1; r < 8; ++r) {
+          a.x += b[r].x; a.y += b[r].y; a.z += b[r].z; a.w += b[r].w;
+        }
         return a;
       };
 #pragma unroll 4
