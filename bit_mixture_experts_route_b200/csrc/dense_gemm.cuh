@@ -97,7 +97,7 @@ struct GemmArgs {
   const float* scale;    // E_STORE: device scalar or null
   int M;
   const void* gu;        // E_SWIGLU_BWD: [M, 2N] gate | up
-  int save;              // E_SWIGLU: write D1
+  int save;              // E_SWIGLU: write D1; E_SWIGLU_BWD: write D0
   int early;             // B is an input of the whole call: load its first stages at once
   int gate_up;           // E_PART: B and the columns as in E_SWIGLU
   float2* stats;         // E_STATS: [2 n_tiles][rows_pad]
@@ -756,30 +756,33 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float2 g2 = unpack2<T>(gw[i]), u2 = unpack2<T>(uw[i]);
-              float hh[2], dg[2], du[2];
+              float si[2], dg[2], du[2];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const float g = e ? g2.y : g2.x, uu = e ? u2.y : u2.x;
                 const float dh = __uint_as_float(v[8 * j + 2 * i + e]);
                 const float sg = sigmoid_fast(g);
-                const float si = g * sg;  // silu(g)
-                hh[e] = si * uu;
-                du[e] = dh * si;
-                dg[e] = dh * uu * (sg + si * (1.0f - sg));
-                ovf |= overflows_out<T>(du[e]) | overflows_out<T>(dg[e]) | overflows_out<T>(hh[e]);
+                si[e] = g * sg;  // silu(g)
+                du[e] = dh * si[e];
+                dg[e] = dh * uu * (sg + si[e] * (1.0f - sg));
+                ovf |= overflows_out<T>(du[e]) | overflows_out<T>(dg[e]);
               }
-              ho[i] = pack2<T>(hh[0], hh[1]);
+              if (p.save) {
+                const float h0 = si[0] * u2.x, h1 = si[1] * u2.y;
+                ovf |= overflows_out<T>(h0) | overflows_out<T>(h1);
+                ho[i] = pack2<T>(h0, h1);
+              }
               go[i] = pack2<T>(dg[0], dg[1]);
               uo[i] = pack2<T>(du[0], du[1]);
             }
-            *reinterpret_cast<uint4*>(d) = make_uint4(ho[0], ho[1], ho[2], ho[3]);
+            if (p.save) *reinterpret_cast<uint4*>(d) = make_uint4(ho[0], ho[1], ho[2], ho[3]);
             *reinterpret_cast<uint4*>(d + STG / 2) = make_uint4(go[0], go[1], go[2], go[3]);
             *reinterpret_cast<uint4*>(d + STG) = make_uint4(uo[0], uo[1], uo[2], uo[3]);
           }
           fence_proxy_async();
           __syncwarp();
           if (lane == 0 && row_w < p.M && col0 < p.N) {
-            tma_store_2d(&dmap0, stg, col0, row_w);
+            if (p.save) tma_store_2d(&dmap0, stg, col0, row_w);
             tma_store_3d(&dmap1, stg + STG / 2, col0, 0, row_w);
             tma_store_3d(&dmap1, stg + STG, col0, 1, row_w);
             bulk_commit();
@@ -936,9 +939,10 @@ struct Plan {
 // microseconds.  A stage costs an SM's way from L2, about 100 GB/s: 0.32 us for
 // the 32 KB of a 256-column tile, 0.25 us for the 24 KB of 128 columns; or, where
 // few row tiles share a column tile, its operands' way from memory at this
-// pair's share of 6.4 TB/s.  A unit costs about 3 us more to fill and drain.
-// Splits cost the joining launch (4 us) and their partial sums' way through L2.
-inline Plan plan_product(int64_t rows, int64_t cols, int k_stages, int most_tiles) {
+// pair's share of 6.4 TB/s.  A unit costs about 2 us more to fill and `epilogue`
+// us per column to drain, which runs under the next unit's stages.  Splits cost the joining launch (4 us) and their partial sums' way through L2.
+inline Plan plan_product(int64_t rows, int64_t cols, int k_stages, int most_tiles,
+                         double epilogue = 0.008) {
   const int pairs = device_pairs(), mt = ceil_div(rows, TILE);
   Plan best = {TILE, 1};
   double best_cost = 1e30;
@@ -952,9 +956,9 @@ inline Plan plan_product(int64_t rows, int64_t cols, int k_stages, int most_tile
       const int kps = ceil_div(k_stages, sp);
       if (ceil_div(k_stages, kps) != sp) continue;  // an empty last split
       const int rounds = ceil_div((int64_t)tiles * sp, pairs);
-      // a round's drain runs under the next one's stages
-      double cost = rounds * kps * stage + 2.0 + 0.004 * tn;
-      if (rounds > 1) cost += (rounds - 1) * std::max(0.0, 0.008 * tn - kps * stage);
+      const double drain = (sp > 1 ? 0.008 : epilogue) * tn;
+      double cost = rounds * kps * stage + 2.0 + drain;
+      cost += (rounds - 1) * std::max(0.0, drain - kps * stage);
       if (sp > 1) cost += 4.0 + 0.015 * tiles * sp;
       if (cost < best_cost) {
         best_cost = cost;
@@ -982,7 +986,7 @@ struct FinishArgs {
   const float* scale;
   const int* row_of;    // F_PLAIN: out row -> row of the sums, -1 for a zero row; or null
   const void* gu;
-  void* out;
+  void* out;            // F_SWIGLU_BWD: h, or null
   void* out1;
   int32_t* dev_err;
 };
@@ -1094,7 +1098,7 @@ __global__ void __launch_bounds__(256 * finish_groups<FIN>()) finish_kernel(Fini
       du[e] = v[e] * sg;
       dg[e] = v[e] * u * (s + sg * (1.0f - s));
     }
-    put(p.out, at, h);
+    if (p.out) put(p.out, at, h);
     put(p.out1, at2, dg);
     put(p.out1, at2 + p.N, du);
   }

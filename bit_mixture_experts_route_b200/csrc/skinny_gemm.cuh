@@ -35,7 +35,7 @@ constexpr int kSkinnyStages = 10; // at most
 enum SkinnyEpilogue {
   S_STORE,       // out[row_of[t] or t] = 16-bit (sum * *scale + residual)
   S_SWIGLU,      // tile = 64 gate rows, 64 up rows: out = h, out1 = gate | up (if given)
-  S_SWIGLU_BWD,  // sums are dh: out = h, out1 = dgate | dup, from gu
+  S_SWIGLU_BWD,  // sums are dh: out = h (if given), out1 = dgate | dup, from gu
   S_STATS,       // per token: loss and lse of the softmax over the columns
   S_DLOGITS,     // out = (exp(sum - lse) - [column is the target]) * row scale
 };
@@ -458,11 +458,15 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
                 h[e] = sg * uu[e];
                 du[e] = v[e] * sg;
                 dg[e] = v[e] * uu[e] * (s + sg * (1.0f - s));
-                ovf |= overflows_out<T>(du[e]) | overflows_out<T>(dg[e]) | overflows_out<T>(h[e]);
+                ovf |= overflows_out<T>(du[e]) | overflows_out<T>(dg[e]);
               }
               T* d = static_cast<T*>(p.out1) + at2;
-              *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at) =
-                  make_uint2(pack2<T>(h[0], h[1]), pack2<T>(h[2], h[3]));
+              if (p.out) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ovf |= overflows_out<T>(h[e]);
+                *reinterpret_cast<uint2*>(static_cast<T*>(p.out) + at) =
+                    make_uint2(pack2<T>(h[0], h[1]), pack2<T>(h[2], h[3]));
+              }
               *reinterpret_cast<uint2*>(d) =
                   make_uint2(pack2<T>(dg[0], dg[1]), pack2<T>(dg[2], dg[3]));
               *reinterpret_cast<uint2*>(d + p.rows) =
