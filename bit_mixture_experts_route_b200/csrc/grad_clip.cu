@@ -12,7 +12,7 @@
 namespace moe {
 namespace {
 
-constexpr int kMaxTensors = 512;  // per launch: 24 bytes each of the 32764 of a launch's parameters
+constexpr int kMaxTensors = 1024;  // per launch: 24 bytes each of the 32764 of a launch's parameters
 constexpr int kThreads = 256;
 constexpr int kChunkBytes = 32768;  // one piece of work, within one tensor
 // Blocks: the squares' are resident all at once (their number is that of the
@@ -365,8 +365,11 @@ cudaError_t grad_norm_clip(const void* const* grads, const int64_t* numel, const
                            int n, float max_norm, void* const* outs, float* norm, void* ws,
                            int32_t* dev_err, cudaStream_t s) {
   double* part = static_cast<double*>(ws);
+  // parameters cost host time by their size: the smallest table that holds all
   if (n <= 64)
     return run<64>(grads, numel, dt, n, max_norm, outs, norm, part, dev_err, s);
+  if (n <= 512)
+    return run<512>(grads, numel, dt, n, max_norm, outs, norm, part, dev_err, s);
   return run<kMaxTensors>(grads, numel, dt, n, max_norm, outs, norm, part, dev_err, s);
 }
 

@@ -251,7 +251,7 @@ def clip_check(grads, max_norm, outs=None, err=None):
 
 @pytest.mark.parametrize("dtype", [torch.float32] + DTYPES)
 @pytest.mark.parametrize("sizes", [[1], [7], [8192], [8193, 0, 1, 16], [100003, 5, 8191, 64] * 3,
-                                   [33] * 65, [1000] * 700])
+                                   [33] * 65, [1000] * 700, [40] * 1100, [9001] * 2100])
 def test_clip_sizes_types_and_places(dtype, sizes):
     g = gen(len(sizes) + sizes[0])
     grads = [randn(g, n, dtype=dtype, sigma=0.1) for n in sizes]
