@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
       tc_fence_after();
       // all CTAs have read the tile before
       if (!__all_sync(0xffffffffu, mbar_wait<true>(&sm.taken, (lt & 1) ^ 1, sm, p.dev_err))) break;
-      for (int c = hc; c < N / 32; c += 2) {
+      for (int c = hc; 32 * c < joined; c += 2) {
         uint32_t v[32];
         tmem_ld32(tmem_base + lane_addr + acc * N + 32 * c, v);
         float* d = sums + (size_t)(32 * c) * CM + 32 * q + lane;
