@@ -774,60 +774,62 @@ def linear_ce_backward(dloss, X, W, targets, lse, ignore_index=-100, need_dx=Tru
     return dX, dW
 
 
-def _apart(grads, outs):
-    """What a call writes overlaps nothing else that it reads or writes: a tensor
-    listed twice would be scaled twice.  An ``out`` may be its gradient itself."""
-    spans = []
-    for i, g in enumerate(grads):
-        if g.numel() == 0:
-            continue
-        a, n = g.data_ptr(), g.numel() * g.element_size()
-        spans.append((a, a + n, f"grads[{i}]", outs is None))
-        if outs is not None and outs[i].data_ptr() != a:
-            spans.append((outs[i].data_ptr(), outs[i].data_ptr() + n, f"outs[{i}]", True))
-        elif outs is not None:
-            spans[-1] = (*spans[-1][:3], True)
-    spans.sort()
-    last = None  # of the spans so far, the one that reaches furthest
-    written = None  # and of the written ones
-    for s in spans:
-        for o in (last if s[3] else None, written):
-            if o is not None and s[0] < o[1]:
-                raise MoEError(f"grad_list: {o[2]} and {s[2]} overlap")
-        if last is None or s[1] > last[1]:
-            last = s
-        if s[3] and (written is None or s[1] > written[1]):
-            written = s
-
-
 class GradList:
     """The gradients of a model as ``grad_norm_clip`` takes them: the host
     arrays of addresses, sizes and types, built once and used every step.  It
     holds the tensors; one whose storage is replaced afterwards (``t.data =``,
-    ``t.set_``) needs a new list."""
+    ``t.set_``) needs a new list.  What a call writes overlaps nothing else that
+    it reads or writes (a tensor listed twice would be scaled twice); an ``out``
+    may be its gradient itself."""
 
     def __init__(self, grads, outs=None):
-        self.grads = list(grads)
-        self.outs = None if outs is None else list(outs)
-        n = len(self.grads)
+        self.grads = grads = list(grads)
+        self.outs = outs = None if outs is None else list(outs)
+        self.n = n = len(grads)
         if n == 0:
             raise MoEError("grad_list: no tensors")
-        if self.outs is not None and len(self.outs) != n:
+        if outs is not None and len(outs) != n:
             raise MoEError("grad_list: one out per gradient")
-        self.device = self.grads[0].device
-        for i, g in enumerate(self.grads):
-            if g.dtype not in DT:
-                raise MoEError(f"grads[{i}] must be fp32, bf16 or fp16, got {g.dtype}")
-            _matrix(g, g.shape, f"grads[{i}]", g.dtype, self.device)
-            if self.outs is not None:
-                _matrix(self.outs[i], g.shape, f"outs[{i}]", g.dtype, self.device)
-        _apart(self.grads, self.outs)
-        self.n = n
-        self._in = (ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads])
-        self._numel = (ctypes.c_int64 * n)(*[g.numel() for g in self.grads])
-        self._dt = (ctypes.c_int * n)(*[DT[g.dtype] for g in self.grads])
-        self._out = None if self.outs is None else \
-            (ctypes.c_void_p * n)(*[o.data_ptr() for o in self.outs])
+        self.device = device = getattr(grads[0], "device", None)
+        for name, ts in (("grads", grads), ("outs", outs or ())):
+            for i, t in enumerate(ts):
+                if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in DT
+                        and t.device == device and t.is_contiguous()):
+                    if isinstance(t, torch.Tensor) and t.dtype not in DT:
+                        raise MoEError(f"{name}[{i}] must be fp32, bf16 or fp16, got {t.dtype}")
+                    _matrix(t, getattr(t, "shape", ()), f"{name}[{i}]",
+                            getattr(t, "dtype", None), device)
+                    raise MoEError(f"{name}[{i}] must be a CUDA tensor")
+        at = [g.data_ptr() for g in grads]
+        numel = [g.numel() for g in grads]
+        ends = [a + k * g.element_size() for a, k, g in zip(at, numel, grads)]
+        if outs is None:
+            spans = [(a, e, 1, i) for i, (a, e) in enumerate(zip(at, ends)) if e > a]
+        else:
+            for i, (g, o) in enumerate(zip(grads, outs)):
+                if o.dtype is not g.dtype or o.shape != g.shape:
+                    _matrix(o, g.shape, f"outs[{i}]", g.dtype, device)
+            to = [o.data_ptr() for o in outs]
+            # (first byte, end, written, place): a gradient, and its out where that
+            # lies elsewhere
+            spans = [(a, e, int(a == o), i) for i, (a, e, o) in enumerate(zip(at, ends, to)) if e > a]
+            spans += [(o, o + e - a, 1, n + i) for i, (a, e, o) in enumerate(zip(at, ends, to))
+                      if e > a and a != o]
+        spans.sort()
+        reach = wreach = (0, -1)  # how far all spans so far, and the written ones, go
+        for a, e, written, i in spans:
+            for end, j in ((reach if written else wreach), wreach):
+                if a < end:
+                    names = [f"grads[{k}]" if k < n else f"outs[{k - n}]" for k in (j, i)]
+                    raise MoEError(f"grad_list: {names[0]} and {names[1]} overlap")
+            if e > reach[0]:
+                reach = (e, i)
+            if written and e > wreach[0]:
+                wreach = (e, i)
+        self._in = (ctypes.c_void_p * n)(*at)
+        self._numel = (ctypes.c_int64 * n)(*numel)
+        self._dt = (ctypes.c_int * n)(*[DT[g.dtype] for g in grads])
+        self._out = None if outs is None else (ctypes.c_void_p * n)(*to)
         self.nbytes = _size("moe_grad_norm_clip_workspace_size", n)
 
 

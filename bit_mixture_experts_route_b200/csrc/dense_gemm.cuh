@@ -959,7 +959,8 @@ inline Plan plan_product(int64_t rows, int64_t cols, int k_stages, int most_tile
       const double drain = (sp > 1 ? 0.008 : epilogue) * tn;
       double cost = rounds * kps * stage + 2.0 + drain;
       cost += (rounds - 1) * std::max(0.0, drain - kps * stage);
-      if (sp > 1) cost += 4.0 + 0.015 * tiles * sp;
+      // the joining launch, longer where it does a long epilogue's work
+      if (sp > 1) cost += 4.0 + 0.015 * tiles * sp + 150.0 * (epilogue - 0.008);
       if (cost < best_cost) {
         best_cost = cost;
         best = {tn, sp};

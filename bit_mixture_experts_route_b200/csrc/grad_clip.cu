@@ -313,7 +313,8 @@ static cudaError_t run(const void* const* grads, const int64_t* numel, const moe
     t.chunk0[0] = 0;
     for (int i = l * CAP; i < std::min(n, (l + 1) * CAP); ++i) {
       if (numel[i] == 0) continue;
-      const int64_t per = chunk_of(dt[i]), c = (numel[i] + per - 1) / per;
+      const uint32_t per = chunk_of(dt[i]);
+      const int64_t c = (int64_t)(((uint64_t)numel[i] + per - 1) / per);
       t.in[t.n] = grads[i];
       t.out[t.n] = outs ? outs[i] : const_cast<void*>(grads[i]);
       t.tail[t.n] = (uint32_t)(numel[i] - (c - 1) * per) | ((uint32_t)dt[i] << 30);
@@ -327,8 +328,8 @@ static cudaError_t run(const void* const* grads, const int64_t* numel, const moe
   };
   Table<CAP> t;
   int parts = 0;
-  int64_t chunks = 0;
-  if (launches == 1 && fill(t, 0) <= kFewPieces) {
+  int64_t chunks = fill(t, 0);
+  if (launches == 1 && chunks <= kFewPieces) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kFewBlocks);
     cfg.blockDim = dim3(kFewThreads);
@@ -345,7 +346,7 @@ static cudaError_t run(const void* const* grads, const int64_t* numel, const moe
     return cudaLaunchKernelEx(&cfg, few_kernel<CAP>, t, max_norm, norm, dev_err);
   }
   for (int l = 0; l < launches; ++l) {
-    chunks = fill(t, l);
+    if (l > 0) chunks = fill(t, l);
     const dim3 b = blocks_of(chunks, kSumBlocks);
     cudaError_t e = launch_pdl(squares_kernel<CAP>, b, dim3(kThreads), 0, s, t, part + parts);
     if (e) return e;
@@ -368,6 +369,8 @@ cudaError_t grad_norm_clip(const void* const* grads, const int64_t* numel, const
   // parameters cost host time by their size: the smallest table that holds all
   if (n <= 64)
     return run<64>(grads, numel, dt, n, max_norm, outs, norm, part, dev_err, s);
+  if (n <= 256)
+    return run<256>(grads, numel, dt, n, max_norm, outs, norm, part, dev_err, s);
   if (n <= 512)
     return run<512>(grads, numel, dt, n, max_norm, outs, norm, part, dev_err, s);
   return run<kMaxTensors>(grads, numel, dt, n, max_norm, outs, norm, part, dev_err, s);
