@@ -677,8 +677,9 @@ def gated_ffn_forward(X, W_gu, W_d, residual=None, save_gu=False, workspace=None
         if gu is None and save_gu:
             gu = X.new_empty((T, 2 * I))
         _check(load().moe_gated_ffn_forward(
-            X.data_ptr(), DT[X.dtype], W_gu.data_ptr(), W_d.data_ptr(), T, H, I, _at(residual), out.data_ptr(),
-            _at(gu), ws.data_ptr(), ws.numel(), _at(dev_err), _raw_stream(dev)), "moe_gated_ffn_forward")
+            X.data_ptr(), DT[X.dtype], W_gu.data_ptr(), W_d.data_ptr(), T, H, I, _at(residual),
+            out.data_ptr(), _at(gu), ws.data_ptr(), ws.numel(), _at(dev_err), _raw_stream(dev)),
+            "moe_gated_ffn_forward")
     return out if gu is None else (out, gu)
 
 
@@ -701,7 +702,8 @@ def gated_ffn_backward(dY, X, gu, W_gu, W_d, need_dx=True, need_dw=True, workspa
         dW_gu = torch.empty_like(W_gu) if need_dw else None
         dW_d = torch.empty_like(W_d) if need_dw else None
         _check(load().moe_gated_ffn_backward(
-            dY.data_ptr(), DT[X.dtype], X.data_ptr(), gu.data_ptr(), W_gu.data_ptr(), W_d.data_ptr(), T, H, I, _at(dX),
+            dY.data_ptr(), DT[X.dtype], X.data_ptr(), gu.data_ptr(), W_gu.data_ptr(),
+            W_d.data_ptr(), T, H, I, _at(dX),
             _at(dW_gu), _at(dW_d), ws.data_ptr(), ws.numel(), _at(dev_err), _raw_stream(dev)),
             "moe_gated_ffn_backward")
     return dX, dW_gu, dW_d
@@ -744,7 +746,8 @@ def linear_ce_forward(X, W, targets, ignore_index=-100, workspace=None, dev_err=
         loss = torch.empty(T, dtype=torch.float32, device=dev)
         lse = torch.empty_like(loss)
         _check(load().moe_linear_ce_forward(
-            X.data_ptr(), DT[X.dtype], W.data_ptr(), targets.data_ptr(), T, H, V, ignore_index, loss.data_ptr(),
+            X.data_ptr(), DT[X.dtype], W.data_ptr(), targets.data_ptr(), T, H, V,
+            ignore_index, loss.data_ptr(),
             lse.data_ptr(), ws.data_ptr(), ws.numel(), _at(dev_err), _raw_stream(dev)),
             "moe_linear_ce_forward")
     return loss, lse
@@ -768,8 +771,9 @@ def linear_ce_backward(dloss, X, W, targets, lse, ignore_index=-100, need_dx=Tru
         dX = torch.empty_like(X) if need_dx else None
         dW = torch.empty_like(W) if need_dw else None
         _check(load().moe_linear_ce_backward(
-            dloss.data_ptr(), X.data_ptr(), DT[X.dtype], W.data_ptr(), targets.data_ptr(), lse.data_ptr(), T, H, V,
-            ignore_index, _at(dX), _at(dW), ws.data_ptr(), ws.numel(), _at(dev_err), _raw_stream(dev)),
+            dloss.data_ptr(), X.data_ptr(), DT[X.dtype], W.data_ptr(), targets.data_ptr(),
+            lse.data_ptr(), T, H, V, ignore_index, _at(dX), _at(dW), ws.data_ptr(), ws.numel(),
+            _at(dev_err), _raw_stream(dev)),
             "moe_linear_ce_backward")
     return dX, dW
 
@@ -812,7 +816,8 @@ class GradList:
             to = [o.data_ptr() for o in outs]
             # (first byte, end, written, place): a gradient, and its out where that
             # lies elsewhere
-            spans = [(a, e, int(a == o), i) for i, (a, e, o) in enumerate(zip(at, ends, to)) if e > a]
+            spans = [(a, e, int(a == o), i) for i, (a, e, o) in enumerate(zip(at, ends, to))
+                     if e > a]
             spans += [(o, o + e - a, 1, n + i) for i, (a, e, o) in enumerate(zip(at, ends, to))
                       if e > a and a != o]
         spans.sort()

@@ -823,7 +823,8 @@ inline bool map_2d(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, in
              std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
              2, const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 template <typename T>
@@ -838,7 +839,8 @@ inline bool map_3d(CUtensorMap* m, const void* p, const int64_t (&d)[3], const i
              std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
              3, const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             b[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             b[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -940,7 +942,8 @@ struct Plan {
 // the 32 KB of a 256-column tile, 0.25 us for the 24 KB of 128 columns; or, where
 // few row tiles share a column tile, its operands' way from memory at this
 // pair's share of 6.4 TB/s.  A unit costs about 2 us more to fill and `epilogue`
-// us per column to drain, which runs under the next unit's stages.  Splits cost the joining launch (4 us) and their partial sums' way through L2.
+// us per column to drain, which runs under the next unit's stages.  Splits cost
+// the joining launch (4 us) and their partial sums' way through L2.
 inline Plan plan_product(int64_t rows, int64_t cols, int k_stages, int most_tiles,
                          double epilogue = 0.008) {
   const int pairs = device_pairs(), mt = ceil_div(rows, TILE);

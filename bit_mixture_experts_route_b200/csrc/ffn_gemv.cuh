@@ -68,7 +68,10 @@ __device__ __forceinline__ uint4 ldg_u4(const void* p) {
 }
 __device__ __forceinline__ float2 lds_cluster2(uint32_t a) {
   float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(a)
+               : "memory");
   return v;
 }
 

@@ -1,7 +1,8 @@
-// Products of a weight matrix with few tokens (17 to 128), on the tensor cores:
+// Products of a weight matrix with few tokens (at most 128), on the tensor cores:
 //   D[t, n] = sum_k X[t, k] W[n, k],  W either way round,
 // the form that the feed-forward block and the vocabulary cross entropy take
-// for a decode batch.  Such a product is bound by reading W once, so the roles
+// for a decode batch (the block's forward pass of a few tokens and not too large
+// weights: ffn_gemv.cuh).  Such a product is bound by reading W once, so the roles
 // of the operands are swapped against dense_gemm.cuh: 128 rows of W are the
 // MMA's M, the tokens its N (32 to 128 columns), and a stage is 16 KB of W with
 // 4 to 16 KB of tokens, where a 256-row tile of mostly absent tokens would
@@ -14,8 +15,14 @@
 // does not depend on timing and nothing goes through global memory or a second
 // launch.  Where even clusters of 8 leave most SMs idle (a short row of W, a long
 // k), several clusters take a slice of k each and leave fp32 sums that a second
-// launch adds in slice order.  Persistent: a cluster walks tiles, and the tensor memory holds two
-// accumulators, so that loads and MMAs of the next tile run under the join.
+// launch adds in slice order.  Persistent: a cluster walks tiles, and the tensor
+// memory holds two accumulators, so that loads and MMAs of the next tile run
+// under the join.
+//
+// Measured: 201 MB of weights at 32 tokens (4096 x 8192, both products) in 45 us,
+// streaming at 6.1 to 6.7 TB/s (a copy: 6.46); the other 13 us are the launches'
+// starts (1 us prologue, 1 to 2 us to the first operands) and the exposed joins
+// (2 us of tensor memory, barriers and distributed shared memory each).
 //
 // Warp roles (384 threads): warp 0 loads (TMA), warp 1 issues the MMAs and owns
 // the tensor memory, warps 4-11 move sums to shared memory (two per TMEM lane
@@ -487,7 +494,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
                                       exp2_approx((v[3] - m) * kLog2e)));
             if (lane == i) {
               const float mn = fmaxf(run_m, m);
-              run_s = run_s * exp2_approx((run_m - mn) * kLog2e) + s * exp2_approx((m - mn) * kLog2e);
+              run_s =
+                  run_s * exp2_approx((run_m - mn) * kLog2e) + s * exp2_approx((m - mn) * kLog2e);
               run_m = mn;
             }
           } else {  // S_DLOGITS
@@ -542,7 +550,8 @@ inline int max_clusters(const void* kern, int c) {
   static std::unordered_map<uint64_t, int> cache;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-  const uint64_t key = (reinterpret_cast<uint64_t>(kern) << 10) ^ (uint64_t)(dev << 4) ^ (uint64_t)c;
+  const uint64_t key =
+      (reinterpret_cast<uint64_t>(kern) << 10) ^ (uint64_t)(dev << 4) ^ (uint64_t)c;
   {
     std::lock_guard<std::mutex> lock(mu);
     const auto it = cache.find(key);

@@ -116,7 +116,8 @@ def test_grad_norm_clip_statuses(c):
     assert call(numel=((1 << 42) + 1,)) == UNSUPPORTED
     assert call(ptrs=(P, P), numel=(1 << 42, 1), dts=(F32, F32)) == UNSUPPORTED
     assert call(nbytes=16) == WORKSPACE
-    assert c.moe_grad_norm_clip(None, None, None, 1, 1.0, None, P, P, 1 << 30, None, None) == INVALID
+    assert c.moe_grad_norm_clip(None, None, None, 1, 1.0, None, P, P, 1 << 30, None,
+                                None) == INVALID
 
 
 # ------------------------------------------------------------- the binding

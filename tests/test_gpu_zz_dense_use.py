@@ -24,7 +24,8 @@ CE = [(2, 64, 300), (33, 264, 40003), (100, 128, 2051), (300, 256, 5003), (2100,
 
 def ffn_case(T, H, I, dtype=torch.bfloat16, seed=0):
     g = gen(T + H + I + seed)
-    return {"X": randn(g, T, H, dtype=dtype), "W_gu": randn(g, 2 * I, H, dtype=dtype, sigma=H ** -0.5),
+    return {"X": randn(g, T, H, dtype=dtype),
+            "W_gu": randn(g, 2 * I, H, dtype=dtype, sigma=H ** -0.5),
             "W_d": randn(g, H, I, dtype=dtype, sigma=I ** -0.5), "R": randn(g, T, H),
             "dY": randn(g, T, H, dtype=dtype)}
 
