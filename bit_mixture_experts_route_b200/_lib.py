@@ -660,7 +660,8 @@ def gated_ffn_forward(X, W_gu, W_d, residual=None, save_gu=False, workspace=None
     (+ residual)`` with ``X [T, H]``, ``W_gu [2I, H]`` (gate rows, then up),
     ``W_d [H, I]``, all bf16 or all fp16, ``residual`` fp32 ``[T, H]``.
     Returns ``Y [T, H]``, or ``(Y, gu)`` when ``save_gu`` or ``gu`` asks for the
-    pre-activations ``[T, 2I]`` that the backward call reads."""
+    pre-activations ``[T, 2I]`` that the backward call reads.  ``out`` and ``gu``
+    must not overlap the inputs."""
     T, H, I = _ffn_shapes(X, W_gu, W_d)
     dev = X.device
     if residual is not None:

@@ -326,6 +326,50 @@ def test_ffn_each_gradient_alone(T):
         assert (close <= 2 * U[torch.bfloat16] * size).all()
 
 
+@pytest.mark.parametrize("T,H,I", [(70001, 64, 72), (2, 65536, 16), (20, 65536, 16),
+                                   (200, 65536, 16), (3, 16, 65536), (130, 16, 65536)])
+def test_ffn_long_in_one_dimension(T, H, I):
+    dtype = torch.bfloat16
+    c = ffn_case(T, H, I)
+    Y, gu = moe.gated_ffn_forward(c["X"], c["W_gu"], c["W_d"], residual=c["R"], save_gu=True)
+    Yr, terms, gur, gterms, _ = ffn_ref(c["X"], c["W_gu"], c["W_d"], c["R"])
+    near(gu, gur, gterms, dtype, 0, "gu")
+    near(Y, Yr, terms, dtype, 1.5, "Y")
+    dX, dWgu, dWd = moe.gated_ffn_backward(c["dY"], c["X"], gu, c["W_gu"], c["W_d"])
+    ga, up = gu.double().chunk(2, 1)
+    sg = torch.sigmoid(ga)
+    dh = c["dY"].double() @ c["W_d"].double()
+    dhs = c["dY"].double().abs() @ c["W_d"].double().abs()
+    ds = sg * (1 + ga * (1 - sg))
+    dgu = torch.cat([dh * up * ds, dh * ga * sg], 1)
+    size = dgu.abs() + (ACC / U[dtype]) * torch.cat(
+        [dhs * (up * ds).abs(), dhs * (ga * sg).abs()], 1) + TINY[dtype] / U[dtype]
+    X, h = c["X"].double(), ga * sg * up
+    near(dX, dgu @ c["W_gu"].double(), size @ c["W_gu"].double().abs(), dtype, 1.5, "dX")
+    near(dWgu, dgu.t() @ X, size.t() @ X.abs(), dtype, 1.5, "dW_gu")
+    near(dWd, c["dY"].double().t() @ h, c["dY"].double().t().abs() @ h.abs(), dtype, 1.5, "dW_d")
+
+
+@pytest.mark.parametrize("T,H,V", [(70001, 64, 300), (5, 65536, 40), (200, 32768, 300)])
+def test_ce_long_in_one_dimension(T, H, V):
+    X, W, y, dl = ce_case(T, H, V, torch.bfloat16, 0.3, 9)
+    loss, lse = moe.linear_ce_forward(X, W, y)
+    rloss, rlse = ce_ref(X, W, y)
+    slack = ACC * (X.double().abs() @ W.double().abs().t()).amax(1) + 2.0 ** -19 * (1 + rlse.abs())
+    slack = torch.where(y >= 0, slack, 0.0)
+    assert ((lse.double() - rlse).abs() <= slack).all()
+    assert ((loss.double() - rloss).abs() <= 2 * slack).all()
+    dX, dW = moe.linear_ce_backward(dl, X, W, y, lse)
+    ref = ce_ref(X, W, y, dl, lse)
+    p = ce_ref(X, W, y, torch.ones_like(dl), lse).abs() + 1
+    lerr = ACC * (X.double().abs() @ W.double().abs().t()) + 2.0 ** -20 * (
+        1 + lse.double().abs())[:, None]
+    size = ref.abs() + lerr * p * dl.double().abs()[:, None] / U[torch.bfloat16]
+    size = torch.where((y >= 0)[:, None], size, 0.0)
+    near(dX, ref @ W.double(), size @ W.double().abs(), torch.bfloat16, 1.01, "dX")
+    near(dW, ref.t() @ X.double(), size.t() @ X.double().abs(), torch.bfloat16, 1.01, "dW")
+
+
 def test_clip_of_nothing_and_limits():
     empty = torch.empty(0, device="cuda")
     assert float(moe.grad_norm_clip([empty, empty[:0]], 1.0)) == 0.0
