@@ -74,6 +74,19 @@ constexpr int stg_of(int epi) {
          : (epi == E_PART || epi == E_STATS) ? 0 : 2 * STG;
 }
 constexpr int stg_bytes(int epi, int tn) { return 4 * halves_of(epi, tn) * stg_of(epi); }
+// Which of the two blocks the store `turn` of a warp's unit number `unit` is
+// staged in, with `turns` stores in a unit (two of 64 columns in a 256-column
+// tile, one in a 128-column tile).  The warp waits for all its stores but the
+// newest, so a store never takes the block of the one before it, which may still
+// be on its way -- over the end of a unit too.
+constexpr int staging_block(int unit, int turn, int turns) { return (unit * turns + turn) & 1; }
+constexpr bool staging_alternates(int turns) {
+  for (int i = 1; i < 4 * turns; ++i)
+    if (staging_block(i / turns, i % turns, turns) ==
+        staging_block((i - 1) / turns, (i - 1) % turns, turns))
+      return false;
+  return true;
+}
 // As many stages as the shared memory holds beside the staging blocks.
 constexpr int kSmemBudget = 227 * 1024 - 1024 - 512;
 constexpr int stages_of(int epi, int tn) {
@@ -620,8 +633,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
         }
 #pragma unroll 1
         for (int blk = 0; blk < CW / 64; ++blk) {
-          // the two staging blocks alternate: this one's last store has left it
-          stg_now = stg + (blk & 1) * STG;
+          // the store before last has left this block; the last one reads the other
+          static_assert(staging_alternates(CW / 64), "a store would be staged over the last one");
+          stg_now = stg + staging_block(lt, blk, CW / 64) * STG;
           if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
           uint32_t w64[2][32];
