@@ -71,6 +71,24 @@ __device__ __forceinline__ uint4 ldg_stream_u4(const void* p) {
   return r;
 }
 
+// The same loads through the coherent path: for what the launch before may have
+// been writing when this kernel started (see pdl_wait below), which read-only
+// loads, here or of __ldg, do not allow for.
+__device__ __forceinline__ uint4 ld_u4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint4 ld_stream_u4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
 // Two bf16 (packed in a u32, element 0 in the low half) -> two fp16.
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v) {
   float lo = __uint_as_float(v << 16);

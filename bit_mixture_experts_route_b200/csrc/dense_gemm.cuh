@@ -516,8 +516,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
         const bool in = r0 + 8 * i < p.M && c < p.N;  // N is a multiple of 8
         const uint4* g = reinterpret_cast<const uint4*>(gp + (size_t)(16 * i) * p.N);
         const uint4* u = reinterpret_cast<const uint4*>(gp + (size_t)(16 * i + 1) * p.N);
-        gu_next[0][i] = in ? ldg_stream_u4(g) : make_uint4(0, 0, 0, 0);
-        gu_next[1][i] = in ? ldg_stream_u4(u) : make_uint4(0, 0, 0, 0);
+        gu_next[0][i] = in ? ld_stream_u4(g) : make_uint4(0, 0, 0, 0);
+        gu_next[1][i] = in ? ld_stream_u4(u) : make_uint4(0, 0, 0, 0);
       }
     };
     // chunk c (16 bytes) of row r in a 64-byte-swizzled block

@@ -57,15 +57,6 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A plain (coherent) load: X is the launch before's output, written while this
-// kernel may already have started, which a read-only load would not allow for.
-__device__ __forceinline__ uint4 ldg_u4(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
-  return r;
-}
 __device__ __forceinline__ float2 lds_cluster2(uint32_t a) {
   float2 v;
   asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];"
@@ -79,12 +70,12 @@ __device__ __forceinline__ float2 lds_cluster2(uint32_t a) {
 // Otherwise out [M, rows] (+ residual), A = W_d [rows, K].  NT: groups of 8
 // tokens.  K and rows are multiples of 8.  The down form is launched right
 // behind the up form, so its weights cannot be anyone's pending output: it
-// loads the first of them before it waits for h.
+// loads the first of them before it waits for h.  Any input may be what the
+// launch before the call has written, so all loads are coherent ones.
 template <typename T, int NT, bool UP, int UNROLL>
 __global__ void __launch_bounds__(32 * kGemvWarps) ffn_gemv_kernel(
-    const T* __restrict__ A, const T* X, int M, int rows, int K,
-    const float* __restrict__ residual, T* __restrict__ out, T* __restrict__ gu,
-    int32_t* dev_err) {
+    const T* A, const T* X, int M, int rows, int K, const float* residual, T* __restrict__ out,
+    T* __restrict__ gu, int32_t* dev_err) {
   __shared__ float sums[kGemvWarps][NT][32][4];
   __shared__ float2 joined[NT][64];
   const int cs = (int)cluster_size(), rank = (int)cluster_rank();
@@ -119,8 +110,8 @@ __global__ void __launch_bounds__(32 * kGemvWarps) ffn_gemv_kernel(
     for (int i = 0; i < UNROLL; ++i) {
       const int k = kGemvK * (c0 + (i >> 1) * kGemvWarps) + 32 * (i & 1);
       const bool in = k + 8 * t < kend;
-      a0[i] = in ? ldg_stream_u4(a0p + k) : zero;
-      a1[i] = in ? ldg_stream_u4(a1p + k) : zero;
+      a0[i] = in ? ld_stream_u4(a0p + k) : zero;
+      a1[i] = in ? ld_stream_u4(a1p + k) : zero;
     }
     if (first) {
       pdl_wait();
@@ -134,7 +125,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps) ffn_gemv_kernel(
       const bool in = k + 8 * t < kend;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const uint4 b = in && live[n] ? ldg_u4(xp[n] + k) : zero;
+        const uint4 b = in && live[n] ? ld_u4(xp[n] + k) : zero;
         mma_16x8x16<T>(acc[n], a0[i].x, a1[i].x, a0[i].y, a1[i].y, b.x, b.y);
         mma_16x8x16<T>(acc[n], a0[i].z, a1[i].z, a0[i].w, a1[i].w, b.z, b.w);
       }

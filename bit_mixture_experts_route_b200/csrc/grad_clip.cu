@@ -103,6 +103,9 @@ __device__ __forceinline__ int head_of(const T* p, int n) {
   return min(h, n);
 }
 
+// (no read-only loads of the gradients: the launch before, a weight gradient or
+// an earlier clipping, may still write them when the kernel starts, and in place
+// the kernel of few pieces writes them itself)
 template <int TH, typename T>
 __device__ __forceinline__ double chunk_squares(const T* p, int n) {
   constexpr int P = per16<T>();
@@ -113,7 +116,7 @@ __device__ __forceinline__ double chunk_squares(const T* p, int n) {
     uint4 r[kSumUnroll];
 #pragma unroll
     for (int j = 0; j < kSumUnroll; ++j)
-      r[j] = i0 + j * TH < vecs ? __ldg(q + i0 + j * TH) : make_uint4(0, 0, 0, 0);
+      r[j] = i0 + j * TH < vecs ? q[i0 + j * TH] : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < kSumUnroll; ++j) {
       if (i0 + j * TH >= vecs) break;
