@@ -606,11 +606,27 @@ def _dev_word(dev_err, device):
 
 
 @functools.lru_cache(maxsize=1024)
-def _size(fn, *args):
-    """The workspace size that ``fn`` gives: a function of the sizes alone."""
+def _size_on(device_index, fn, *args):
     n = ctypes.c_size_t()
     _check(getattr(load(), fn)(*args, ctypes.byref(n)), fn)
     return n.value
+
+
+def _size(fn, *args):
+    """The workspace size that ``fn`` gives: a function of the sizes and of the
+    current device, whose number of SMs the split of the work follows."""
+    try:
+        index = _current_device()
+    except RuntimeError:  # no device: the sizes for a B200
+        index = None
+    return _size_on(index, fn, *args)
+
+
+def _size_for(device, fn, *args):
+    if device is None:
+        return _size(fn, *args)
+    with _on(torch.device(device)):
+        return _size(fn, *args)
 
 
 def _space(workspace, nbytes, device):
@@ -622,12 +638,14 @@ def _space(workspace, nbytes, device):
     return workspace
 
 
-def gated_ffn_forward_workspace_size(T, H, I):
-    return _size("moe_gated_ffn_forward_workspace_size", T, H, I)
+def gated_ffn_forward_workspace_size(T, H, I, device=None):
+    """Bytes that a call on ``device`` (default: the current one) needs."""
+    return _size_for(device, "moe_gated_ffn_forward_workspace_size", T, H, I)
 
 
-def gated_ffn_backward_workspace_size(T, H, I):
-    return _size("moe_gated_ffn_backward_workspace_size", T, H, I)
+def gated_ffn_backward_workspace_size(T, H, I, device=None):
+    """Bytes that a call on ``device`` (default: the current one) needs."""
+    return _size_for(device, "moe_gated_ffn_backward_workspace_size", T, H, I)
 
 
 def _ffn_shapes(X, W_gu, W_d):
@@ -710,12 +728,14 @@ def gated_ffn_backward(dY, X, gu, W_gu, W_d, need_dx=True, need_dw=True, workspa
     return dX, dW_gu, dW_d
 
 
-def linear_ce_forward_workspace_size(T, H, V):
-    return _size("moe_linear_ce_forward_workspace_size", T, H, V)
+def linear_ce_forward_workspace_size(T, H, V, device=None):
+    """Bytes that a call on ``device`` (default: the current one) needs."""
+    return _size_for(device, "moe_linear_ce_forward_workspace_size", T, H, V)
 
 
-def linear_ce_backward_workspace_size(T, H, V):
-    return _size("moe_linear_ce_backward_workspace_size", T, H, V)
+def linear_ce_backward_workspace_size(T, H, V, device=None):
+    """Bytes that a call on ``device`` (default: the current one) needs."""
+    return _size_for(device, "moe_linear_ce_backward_workspace_size", T, H, V)
 
 
 def _ce_shapes(X, W, targets, ignore_index):

@@ -39,6 +39,9 @@
  *   an expert index out of range) set a bit in the caller's device word
  *   `dev_err` (int32, may be NULL) and the affected work is skipped; the
  *   caller reads the word when it chooses.  No kernel traps or asserts.
+ * - A workspace size follows from the sizes that it is asked for and, in the
+ *   dense training-side calls, from the number of SMs: ask for it with the
+ *   device current that the call will run on.
  * - sm_100a only: calls on another architecture return MOE_ERR_UNSUPPORTED.
  *
  * NF4 weight layout (the fused 3-D expert parameter of "4-bit
