@@ -104,7 +104,7 @@ struct GemmArgs {
   // reduction (dyn = 2); a multiple of 256 rows is readable either way
   const int* rows;
   int dyn;
-  float* part;           // E_PART: [split][tile][256][256]
+  float* part;           // E_PART: [split][tile][256][256], the tiles of *rows
   int accumulate;        // E_PART: add to what is there
   const float* residual; // E_STORE: fp32 [rows, N] or null
   const float* scale;    // E_STORE: device scalar or null
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
       if constexpr (EPI == E_PART) {
         const int tile = w.mt * p.n_tiles + w.nt;
         float* dst = p.part +
-                     ((size_t)w.split * p.m_tiles * p.n_tiles + tile) * (size_t)TILE_FLOATS +
+                     ((size_t)w.split * m_tiles * p.n_tiles + tile) * (size_t)TILE_FLOATS +
                      (rank * CM + 32 * q + lane);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -998,7 +998,8 @@ struct FinishArgs {
   const float* part;  // [split][tile][256 columns][256 rows]
   int splits, n_tiles;
   const int* splits_of;  // device word with the splits, or null
-  size_t split_stride;  // floats
+  size_t split_stride;  // floats; or, with `rows` (device), that of so many rows' tiles
+  const int* rows;
   int M, N;             // rows and columns of out
   const float* residual;
   const float* scale;
@@ -1038,9 +1039,11 @@ __global__ void __launch_bounds__(256 * finish_groups<FIN>()) finish_kernel(Fini
                        (size_t)(col + warp) * TILE + (cr & 255);
     float a[8] = {}, b[8] = {};
     if (cr >= 0) {
-      src += (size_t)grp * p.split_stride;
+      size_t stride = p.split_stride;
+      if (p.rows) stride = (size_t)((*p.rows + TILE - 1) / TILE) * p.n_tiles * TILE_FLOATS;
+      src += (size_t)grp * stride;
 #pragma unroll 4
-      for (int sp = grp; sp < splits; sp += G, src += G * p.split_stride) {
+      for (int sp = grp; sp < splits; sp += G, src += G * stride) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           a[i] += src[(size_t)(8 * i) * TILE];

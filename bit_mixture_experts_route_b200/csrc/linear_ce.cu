@@ -29,7 +29,11 @@ namespace {
 using namespace dense;
 
 constexpr size_t kPieceBytes = (size_t)256 << 20;  // of dl
-constexpr int kPartTiles = 148;
+// dX's fp32 sums: at most so many tiles of 256 KB for the splits of its
+// reduction, unless one copy is more.  Splits are worth their sums where the
+// tiles of the rows that count leave a part-filled last round, so their number is
+// chosen on the device within this room.
+constexpr int kPartTiles = 1024;
 
 struct Meta {
   int rows;         // that count
@@ -49,7 +53,8 @@ struct GatherArgs {
   const float* lse_in;
   float in_unit;
   Meta* meta;
-  int n_tiles, k_stages, most_splits, pairs;  // of dX's reduction; most_splits 0: none
+  // of dX's reduction; most_splits 0: none
+  int n_tiles, k_stages, most_splits, part_tiles, pairs;
   int* inv;
   int* row_of;
   uint4* Xc;
@@ -130,8 +135,9 @@ __device__ __forceinline__ Count count_rows(const GatherArgs& p, int first) {
   }
   if (blockIdx.x == 0 && tid < EPI_NW * 8) p.meta->arrived[tid] = 0;
   if (blockIdx.x == 0 && warp == 1 && p.most_splits > 0) {
-    const int sp =
-        even_splits((c.all + TILE - 1) / TILE * p.n_tiles, p.k_stages, p.most_splits, p.pairs);
+    const int tiles = (c.all + TILE - 1) / TILE * p.n_tiles;
+    const int most = min(p.most_splits, p.part_tiles / max(tiles, 1));
+    const int sp = even_splits(tiles, p.k_stages, most, p.pairs);
     if (lane == 0) p.meta->splits = sp;
   }
   if (blockIdx.x == 0 && bad) set_dev_err(p.dev_err, MOE_DEVERR_BAD_INDEX);
@@ -320,7 +326,7 @@ size_t align1k(size_t b) { return (b + 1023) & ~(size_t)1023; }
 // Layout of both workspaces.
 struct Space {
   size_t meta, inv, row_of, ctarget, clse, cscale, xc, stats, tsum, dl, part, total;
-  int rows_pad, piece, pieces, most_splits;
+  int rows_pad, piece, pieces, most_splits, part_tiles;
   bool skinny;  // few rows, one piece: skinny_gemm.cuh
 };
 // Vocabulary columns of one piece: dl of all rows within kPieceBytes, the
@@ -358,8 +364,10 @@ Space space_of(int T, int H, int V, bool backward) {
       w.part = take(skinny_part_bytes(T, H, V));
     } else {
       const int tiles = w.rows_pad / TILE * ceil_div(H, TILE);
-      w.most_splits = std::min(16, std::max(4, kPartTiles / tiles));
-      w.part = take((size_t)w.most_splits * tiles * TILE_FLOATS * 4);
+      // few tiles: up to two units per pair of a B200
+      w.most_splits = std::min(16, std::max(4, 148 / tiles));
+      w.part_tiles = std::min(w.most_splits * tiles, std::max(tiles, kPartTiles));
+      w.part = take((size_t)w.part_tiles * TILE_FLOATS * 4);
     }
   }
   w.total = at;
@@ -386,6 +394,7 @@ cudaError_t gather(const Space& w, char* ws, const void* X, const void* W, const
   g.n_tiles = ceil_div(H, TILE);
   g.k_stages = w.piece / GK;
   g.most_splits = w.most_splits;
+  g.part_tiles = w.part_tiles;
   g.pairs = device_pairs();
   g.inv = reinterpret_cast<int*>(ws + w.inv);
   g.row_of = reinterpret_cast<int*>(ws + w.row_of);
@@ -572,7 +581,7 @@ cudaError_t backward(const float* dloss, const void* X, const void* W, const int
   f.part = part;
   f.splits_of = &meta->splits;
   f.n_tiles = ht;
-  f.split_stride = (size_t)mt * ht * TILE_FLOATS;
+  f.rows = &meta->rows;
   f.M = rows;
   f.N = H;
   f.scale = &meta->out_scale;

@@ -621,7 +621,8 @@ moe_status_t moe_gated_ffn_backward(const void* dY, moe_dtype_t dtype, const voi
  *             outside [0, V) sets MOE_DEVERR_BAD_INDEX and is treated the same
  *   loss, lse fp32 [T]
  *   dev_err   int32 device word or NULL: BAD_INDEX, TIMEOUT
- * Sums, maxima and exponentials are fp32.  Pointers 16-byte aligned.
+ * Sums, maxima and exponentials are fp32.  Pointers 16-byte aligned.  The
+ * workspace holds X's rows once more and, beyond 128 rows, T V / 16 bytes.
  */
 moe_status_t moe_linear_ce_forward_workspace_size(int T, int H, int V, size_t* bytes);
 moe_status_t moe_linear_ce_forward(const void* X, moe_dtype_t dtype, const void* W,
@@ -635,7 +636,10 @@ moe_status_t moe_linear_ce_forward(const void* X, moe_dtype_t dtype, const void*
  *   dl[t, v] = (exp(l[t, v] - lse[t]) - [v == targets[t]]) * dloss[t],
  *   dX = dl W [T, H],  dW = dl^T X [V, H]   (both of dtype; one may be NULL)
  * The vocabulary is taken in pieces whose dl (16 bits) fits 256 MB of the
- * workspace; the logits of a piece are computed again.  Ignored rows give zero
+ * workspace (at least 256 columns, so 512 T bytes beyond 2^19 rows); the logits
+ * of a piece are computed again.  With it the workspace holds X's rows once more
+ * and dX's fp32 sums: 4 T H bytes (T and H rounded up to 256), or several copies
+ * within 256 MB; whether or not dX is asked for.  Ignored rows give zero
  * rows of dX and nothing to dW.  dl is rounded once to dtype relative to
  * max |dloss| (the products' operand); sums are fp32, each gradient is rounded
  * once.  dev_err: BAD_INDEX, RANGE (an F16 gradient overflowed), TIMEOUT.

@@ -67,3 +67,13 @@ def test_a_size_for_another_device(lib, op):
 def test_a_size_without_a_device():
     # the library is the built one; no GPU is needed to ask
     assert _lib.linear_ce_backward_workspace_size(4, 64, 64) > 0
+
+
+@pytest.mark.parametrize("T,H,V", [(4096, 2048, 151936), (5000, 3840, 19000), (17000, 4096, 8000),
+                                   (65536, 4096, 151936), (1 << 20, 4096, 32000), (300, 64, 70),
+                                   (129, 16384, 1 << 20)])
+def test_room_of_the_cross_entropy_backward(T, H, V):
+    # the rows once more, a piece of dl, dX's sums, and what there is per row
+    rows, wide, mb256 = (T + 255) // 256 * 256, (H + 255) // 256 * 256, 256 << 20
+    most = 2 * rows * H + max(mb256, 512 * rows) + max(mb256, 4 * rows * wide) + 64 * rows + 65536
+    assert _lib.linear_ce_backward_workspace_size(T, H, V) <= most
