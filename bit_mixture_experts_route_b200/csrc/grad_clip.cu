@@ -5,6 +5,8 @@
 // launches: every block sums the squares of its share of the elements and
 // leaves one double; every block of the second adds those in the same fixed
 // order (so all agree, and a run repeats bit for bit) and scales its share.
+// Which elements add up in fp32 first follows from the 16-byte boundaries of
+// memory: the same values at another offset may differ in the last bits.
 // The tensors' addresses travel in the launch's parameters, up to kMaxTensors
 // per launch, so a captured graph holds them and no device table is needed.
 // Bound by memory: 1.02e9 bf16 elements in 290 tensors take 967 us, the three

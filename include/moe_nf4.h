@@ -670,8 +670,10 @@ moe_status_t moe_linear_ce_backward(const float* dloss, const void* X, moe_dtype
  *             infinity, the clipping still uses its fp64 value
  *   dev_err   MOE_DEVERR_NONFINITE when the norm is not finite (an element is
  *             NaN or infinite); the factor is then 1
- * Squares are added in fp32 per eight elements and in fp64 from there, in an
- * order that depends on the sizes only: the same input gives the same bits.
+ * Squares are added in fp32 per 16 bytes (four or eight elements) and in fp64
+ * from there, in an order that depends on the sizes and on where each tensor
+ * begins modulo 16 bytes: the same input there gives the same bits, at another
+ * offset the last bits of the norm may differ.
  * workspace 16-byte aligned, moe_grad_norm_clip_workspace_size bytes.
  */
 moe_status_t moe_grad_norm_clip_workspace_size(int n, size_t* bytes);

@@ -126,3 +126,23 @@ def test_block_behind_the_gathering_of_its_inputs(T, H, I):
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert all(torch.equal(x, y) for x, y in zip(a, b, strict=True))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16, torch.float16])
+@pytest.mark.parametrize("n", [777, 50001, 3_000_017])
+def test_norm_repeats_at_equal_offsets(n, dtype):
+    # the order of the sum follows from the sizes and the offsets modulo 16 bytes
+    g = gen(n)
+    per = 16 // dtype.itemsize
+    values = randn(g, n, dtype=dtype, sigma=0.1)
+    ref = math.sqrt(float(values.double().square().sum()))
+    for off in (0, 1, per - 1):
+        seen = []
+        for base in (0, 3 * per, 40 * per):  # other addresses, the same offset
+            flat = torch.zeros(n + 50 * per, dtype=dtype, device="cuda")
+            t = flat[base + off:base + off + n]
+            t.copy_(values)
+            norm = moe.grad_norm_clip([t], 0.5 * ref)
+            assert abs(float(norm) - ref) <= 6 * 2.0 ** -24 * ref
+            seen.append((norm, t.clone()))
+        assert all(torch.equal(a, seen[0][0]) and torch.equal(b, seen[0][1]) for a, b in seen)
