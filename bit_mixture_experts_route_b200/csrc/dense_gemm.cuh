@@ -188,6 +188,16 @@ __device__ __forceinline__ float sigmoid_fast(float x) {
   return r;
 }
 
+// The activation backward of h = silu(g) u for the gradient dh of h, with
+// s = sigmoid(g): dg = dh u s (1 + g (1 - s)), du = dh g s; and h again.
+struct SwigluGrad {
+  float h, dg, du;
+};
+__device__ __forceinline__ SwigluGrad swiglu_grad(float dh, float g, float u) {
+  const float s = sigmoid_fast(g), silu = g * s;
+  return {silu * u, dh * u * (s + silu * (1.0f - s)), dh * silu};
+}
+
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map,
                                                  uint32_t cluster_bar, int x, int y, int z) {
   asm volatile(
@@ -770,24 +780,16 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) dense_gemm_kernel(
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float2 g2 = unpack2<T>(gw[i]), u2 = unpack2<T>(uw[i]);
-              float si[2], dg[2], du[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float g = e ? g2.y : g2.x, uu = e ? u2.y : u2.x;
-                const float dh = __uint_as_float(v[8 * j + 2 * i + e]);
-                const float sg = sigmoid_fast(g);
-                si[e] = g * sg;  // silu(g)
-                du[e] = dh * si[e];
-                dg[e] = dh * uu * (sg + si[e] * (1.0f - sg));
-                ovf |= overflows_out<T>(du[e]) | overflows_out<T>(dg[e]);
-              }
+              const SwigluGrad a = swiglu_grad(__uint_as_float(v[8 * j + 2 * i]), g2.x, u2.x);
+              const SwigluGrad b = swiglu_grad(__uint_as_float(v[8 * j + 2 * i + 1]), g2.y, u2.y);
+              ovf |= overflows_out<T>(a.du) | overflows_out<T>(a.dg);
+              ovf |= overflows_out<T>(b.du) | overflows_out<T>(b.dg);
               if (p.save) {
-                const float h0 = si[0] * u2.x, h1 = si[1] * u2.y;
-                ovf |= overflows_out<T>(h0) | overflows_out<T>(h1);
-                ho[i] = pack2<T>(h0, h1);
+                ovf |= overflows_out<T>(a.h) | overflows_out<T>(b.h);
+                ho[i] = pack2<T>(a.h, b.h);
               }
-              go[i] = pack2<T>(dg[0], dg[1]);
-              uo[i] = pack2<T>(du[0], du[1]);
+              go[i] = pack2<T>(a.dg, b.dg);
+              uo[i] = pack2<T>(a.du, b.du);
             }
             if (p.save) *reinterpret_cast<uint4*>(d) = make_uint4(ho[0], ho[1], ho[2], ho[3]);
             *reinterpret_cast<uint4*>(d + STG / 2) = make_uint4(go[0], go[1], go[2], go[3]);
@@ -943,6 +945,7 @@ cudaError_t launch_gemm(const Operand& a, const Operand& b, const CUtensorMap& d
 }
 
 inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+inline size_t align1k(size_t b) { return (b + 1023) & ~(size_t)1023; }
 
 // Pairs of CTAs of the current device (two SMs each), as the plans count them.
 inline int device_pairs() { return std::max(1, device_sm_count() / 2); }
@@ -1113,11 +1116,11 @@ __global__ void __launch_bounds__(256 * finish_groups<FIN>()) finish_kernel(Fini
     float h[8], dg[8], du[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float g = to_f32<T>(gu[at2 + e]), u = to_f32<T>(gu[at2 + p.N + e]);
-      const float s = sigmoid_fast(g), sg = g * s;
-      h[e] = sg * u;
-      du[e] = v[e] * sg;
-      dg[e] = v[e] * u * (s + sg * (1.0f - s));
+      const SwigluGrad r =
+          swiglu_grad(v[e], to_f32<T>(gu[at2 + e]), to_f32<T>(gu[at2 + p.N + e]));
+      h[e] = r.h;
+      dg[e] = r.dg;
+      du[e] = r.du;
     }
     if (p.out) put(p.out, at, h);
     put(p.out1, at2, dg);

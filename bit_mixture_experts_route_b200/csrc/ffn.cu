@@ -40,7 +40,6 @@ size_t part_bytes(int64_t rows, int64_t cols, const Plan& pl) {
 size_t part_bytes(int64_t rows, int64_t cols, int64_t K) {
   return part_bytes(rows, cols, plan_of(rows, cols, K));
 }
-size_t align1k(size_t b) { return (b + 1023) & ~(size_t)1023; }
 
 void set_plan(GemmArgs& a, int64_t rows, int64_t cols, int64_t K, Plan pl) {
   a.m_tiles = ceil_div(rows, TILE);

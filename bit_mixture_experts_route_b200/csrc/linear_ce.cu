@@ -33,7 +33,7 @@ constexpr size_t kPieceBytes = (size_t)256 << 20;  // of dl
 // reduction, unless one copy is more.  Splits are worth their sums where the
 // tiles of the rows that count leave a part-filled last round, so their number is
 // chosen on the device within this room.
-constexpr int kPartTiles = 1024;
+constexpr int kSumTiles = 1024;
 
 struct Meta {
   int rows;         // that count
@@ -321,8 +321,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) ce_join_kernel(
   }
 }
 
-size_t align1k(size_t b) { return (b + 1023) & ~(size_t)1023; }
-
 // Layout of both workspaces.
 struct Space {
   size_t meta, inv, row_of, ctarget, clse, cscale, xc, stats, tsum, dl, part, total;
@@ -366,7 +364,7 @@ Space space_of(int T, int H, int V, bool backward) {
       const int tiles = w.rows_pad / TILE * ceil_div(H, TILE);
       // few tiles: up to two units per pair of a B200
       w.most_splits = std::min(16, std::max(4, 148 / tiles));
-      w.part_tiles = std::min(w.most_splits * tiles, std::max(tiles, kPartTiles));
+      w.part_tiles = std::min(w.most_splits * tiles, std::max(tiles, kSumTiles));
       w.part = take((size_t)w.part_tiles * TILE_FLOATS * 4);
     }
   }

@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
   SkinnyBars& sm = *reinterpret_cast<SkinnyBars*>(ring + NS * STAGE + skinny_sums(N));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank(), cs = (int)cluster_size();
-  const uint32_t tmem_cols = N <= 16 ? 32u : N <= 32 ? 64u : N <= 64 ? 128u : 256u;
+  const uint32_t tmem_cols = N <= 32 ? 64u : N <= 64 ? 128u : 256u;  // two accumulators
 
   if (threadIdx.x == 0) {
     prefetch_map(&wmap);
@@ -461,10 +461,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) skinny_gemm_kernel(
               float h[4], dg[4], du[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float s = sigmoid_fast(g[e]), sg = g[e] * s;
-                h[e] = sg * uu[e];
-                du[e] = v[e] * sg;
-                dg[e] = v[e] * uu[e] * (s + sg * (1.0f - s));
+                const SwigluGrad r = swiglu_grad(v[e], g[e], uu[e]);
+                h[e] = r.h;
+                dg[e] = r.dg;
+                du[e] = r.du;
                 ovf |= overflows_out<T>(du[e]) | overflows_out<T>(dg[e]);
               }
               T* d = static_cast<T*>(p.out1) + at2;
