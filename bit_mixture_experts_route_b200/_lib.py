@@ -758,7 +758,9 @@ def linear_ce_forward(X, W, targets, ignore_index=-100, workspace=None, dev_err=
     """Cross entropy of the softmax over ``X W^T`` without keeping it: ``X [T,
     H]``, ``W [V, H]`` (both bf16 or both fp16), ``targets`` int32 ``[T]`` ->
     ``(loss fp32 [T], lse fp32 [T])``, both 0 in rows whose target is
-    ``ignore_index``."""
+    ``ignore_index``.  All addresses are multiples of 16 bytes, so a shifted view
+    such as ``labels[1:]`` needs a copy (``labels[1:].int()`` of int64 labels is
+    one)."""
     T, H, V = _ce_shapes(X, W, targets, ignore_index)
     dev = X.device
     _dev_word(dev_err, dev)
@@ -801,8 +803,12 @@ def linear_ce_backward(dloss, X, W, targets, lse, ignore_index=-100, need_dx=Tru
 
 class GradList:
     """The gradients of a model as ``grad_norm_clip`` takes them: the host
-    arrays of addresses, sizes and types, built once and used every step.  It
-    holds the tensors; one whose storage is replaced afterwards (``t.data =``,
+    arrays of addresses, sizes and types, built once and used every step.
+    Building it takes about 1 us per tensor, 2 us with ``outs`` (224 tensors:
+    0.2 and 0.4 ms), against 10 to 20 us for the host side of a call: it pays where
+    the gradients keep their storage (zeroed in place, views of one buffer), and
+    is part of every step where they are new tensors each time.  It holds the
+    tensors; one whose storage is replaced afterwards (``t.data =``,
     ``t.set_``) needs a new list.  What a call writes overlaps nothing else that
     it reads or writes (a tensor listed twice would be scaled twice); an ``out``
     may be its gradient itself."""

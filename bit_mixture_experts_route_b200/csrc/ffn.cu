@@ -12,8 +12,8 @@
 // (and h again, for dW_d) into the epilogue of dY Wd; both weight gradients are
 // one list of tiles.  Where tiles alone leave SMs idle a product is split along k
 // and one more launch joins it.
-// Measured (bf16, 4096 tokens, 2048 x 8192): forward 345 us = 1.20 PFLOP/s,
-// backward 724 us = 1.14, under the power cap; a library GEMM sustains 1.39.
+// Measured (bf16, 4096 tokens, 2048 x 8192): forward 343 us = 1.20 PFLOP/s,
+// backward 721 us = 1.14, under the power cap; a library GEMM sustains 1.39.
 #include "ffn_gemv.cuh"
 #include "skinny_gemm.cuh"
 

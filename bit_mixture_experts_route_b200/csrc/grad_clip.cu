@@ -9,8 +9,8 @@
 // memory: the same values at another offset may differ in the last bits.
 // The tensors' addresses travel in the launch's parameters, up to kMaxTensors
 // per launch, so a captured graph holds them and no device table is needed.
-// Bound by memory: 1.02e9 bf16 elements in 290 tensors take 967 us, the three
-// passes over 2.04 GB (read; read and write) at 6.4 TB/s, 6.6 within the kernels.
+// Bound by memory: 1.02e9 bf16 elements in 290 tensors take 969 us, the three
+// passes over 2.04 GB (read; read and write) at 6.3 TB/s, 6.6 within the kernels.
 #include "tc_ops.cuh"
 
 namespace moe {
@@ -19,8 +19,10 @@ namespace {
 constexpr int kMaxTensors = 1024;  // per launch: 24 of the 32764 bytes of parameters each
 constexpr int kThreads = 256;
 constexpr int kChunkBytes = 32768;  // one piece of work, within one tensor
-// Blocks: the squares' are resident all at once (their number is that of the
-// partial sums); the scaling's are many, which keeps reads and writes mixed.
+// Blocks, in multiples of a B200's SMs: the squares' are resident all at once
+// there (their number is that of the partial sums, so it is fixed: the sum's order
+// must not follow from the device); the scaling's are many, which keeps reads and
+// writes mixed.
 constexpr int kSumBlocks = 148 * 6, kScaleBlocks = 148 * 128;
 // elements of a chunk: 16-bit types 16384, fp32 8192
 __host__ __device__ constexpr int chunk_of(uint32_t dt) {

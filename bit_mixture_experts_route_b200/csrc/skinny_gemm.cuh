@@ -20,9 +20,12 @@
 // under the join.
 //
 // Measured: 201 MB of weights at 32 tokens (4096 x 8192, both products) in 45 us,
-// streaming at 6.1 to 6.7 TB/s (a copy: 6.46); the other 13 us are the launches'
-// starts (1 us prologue, 1 to 2 us to the first operands) and the exposed joins
-// (2 us of tensor memory, barriers and distributed shared memory each).
+// 4.5 TB/s over the whole call (a copy: 6.46).  The two kernels alone, caches cold,
+// take 30 us for 134 MB and 20 us for 67 MB: a fixed part of about 10 us each (the
+// start, the way to the first operands, the last tile's join, the end) beside
+// the stream, of which the chained launch hides some.  A CTA takes all of an SM's
+// shared memory, so the next launch's CTAs are set up only where this one's have
+// left.
 //
 // Warp roles (384 threads): warp 0 loads (TMA), warp 1 issues the MMAs and owns
 // the tensor memory, warps 4-11 move sums to shared memory (two per TMEM lane

@@ -33,6 +33,8 @@
  *   stream).  Every call only enqueues work: it is asynchronous and
  *   stream-ordered, and never synchronizes the device.
  * - Matrices are dense and row-major.  Sizes are element counts.
+ * - Unless a call says otherwise, its outputs and its workspace overlap
+ *   neither its inputs nor one another.
  * - Synchronous argument errors return at once and enqueue nothing.
  *   A launch failure returns MOE_ERR_CUDA.  Contract violations that only
  *   the device can see (non-finite weights, inconsistent expert offsets,
@@ -639,10 +641,11 @@ moe_status_t moe_linear_ce_forward(const void* X, moe_dtype_t dtype, const void*
  * workspace (at least 256 columns, so 512 T bytes beyond 2^19 rows); the logits
  * of a piece are computed again.  With it the workspace holds X's rows once more
  * and dX's fp32 sums: 4 T H bytes (T and H rounded up to 256), or several copies
- * within 256 MB; whether or not dX is asked for.  Ignored rows give zero
- * rows of dX and nothing to dW.  dl is rounded once to dtype relative to
- * max |dloss| (the products' operand); sums are fp32, each gradient is rounded
- * once.  dev_err: BAD_INDEX, RANGE (an F16 gradient overflowed), TIMEOUT.
+ * within 256 MB; whether or not dX is asked for.  Ignored rows give zero rows
+ * of dX and nothing to dW.  dl is rounded once to dtype relative to max |dloss|
+ * (the products' operand; in F16 to 11 bits down to 2^-29 of that maximum and to
+ * a step of 2^-39 of it below); sums are fp32, each gradient is rounded once.
+ * dev_err: BAD_INDEX, RANGE (an F16 gradient overflowed), TIMEOUT.
  * T == 0 zeroes dW.
  */
 moe_status_t moe_linear_ce_backward_workspace_size(int T, int H, int V, size_t* bytes);
